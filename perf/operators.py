@@ -1,0 +1,411 @@
+"""Cases of the paged KV cache's operators: the plan of a serving step (block
+tables and slot maps from the requests' lengths), the write of the new K and V
+rows into the pages, and the attention of the new tokens over the cache.
+
+A request s holds ctx[s] tokens in the cache and brings new[s] rows to the
+step; the rows of all requests are packed one behind the other.  The lengths
+of a case follow from the case alone (`lens` seeds them), the tensors' values
+and the pages' places from prepare()'s seed.
+"""
+
+import math
+
+import numpy as np
+import torch
+
+own = False
+
+DEV = "cuda"
+TYPES = {"bf16": torch.bfloat16, "fp32": torch.float32}
+
+
+# ------------------------------------------------------------------ the cases
+
+def _case(name, op, S, ctx, new, page, Hq=32, Hkv=8, d=128, dtype="bf16", window=0, chunks=0, pad=0, lens=1):
+    """ctx, new: (least, most); `chunks` > 0: that many requests bring `new` rows and every other one a single row."""
+    return {"name": name, "op": op, "S": S, "ctx_lo": ctx[0], "ctx_hi": ctx[1], "new_lo": new[0], "new_hi": new[1],
+            "page": page, "Hq": Hq, "Hkv": Hkv, "d": d, "dtype": dtype, "window": window, "chunks": chunks,
+            "pad": pad, "lens": lens}
+
+
+def listed():
+    return [
+        # the smallest calls: a decode batch's plan and write, one sequence's token; latency is what counts
+        _case("plan_decode", "plan", 64, (1, 8191), (1, 1), 64, lens=11),
+        _case("append_decode", "append", 64, (1, 2047), (1, 1), 64, lens=12),
+        _case("attn_one_token", "attn", 1, (999, 999), (1, 1), 64, lens=13),
+        # many ragged prompts at once, small pages; rows behind the last prompt pad the batch
+        _case("plan_prompts", "plan", 512, (0, 32767), (0, 127), 16, pad=77, lens=14),
+        _case("append_prompts", "append", 24, (0, 2047), (1, 1365), 16, pad=5, lens=15),
+        # an odd number of narrow heads in 32 bits
+        _case("append_fp32", "append", 7, (0, 999), (1, 500), 32, Hq=3, Hkv=3, d=64, dtype="fp32", lens=16),
+        # decode batches: short ragged sequences on small pages; the long-context batch of 16 sequences,
+        # 32 query and 8 KV heads, up to 131072 tokens
+        _case("attn_decode_ragged", "attn", 128, (0, 8191), (1, 1), 16, lens=17),
+        _case("attn_decode_long", "attn", 16, (65535, 131071), (1, 1), 64, lens=18),
+        # one large chunk of a long prompt
+        _case("attn_chunk", "attn", 1, (16001, 16001), (4096, 4096), 128, lens=19),
+        # a batch that mixes chunks of prompts with decoding sequences, 6 query heads to a KV head
+        _case("attn_mixed", "attn", 24, (0, 6000), (100, 700), 32, Hq=12, Hkv=2, chunks=4, pad=3, lens=20),
+        # sliding window, one query head per KV head, d = 64
+        _case("attn_window", "attn", 3, (0, 9000), (600, 1500), 16, Hq=8, Hkv=8, d=64, window=1000, lens=21),
+        # 32-bit reference precision
+        _case("attn_fp32", "attn", 5, (0, 2000), (1, 130), 16, Hq=6, Hkv=2, d=64, dtype="fp32", lens=22),
+    ]
+
+
+def _log_int(rng, lo, hi):
+    return max(lo, min(hi, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi + 1)))))))
+
+
+def draw(rng):
+    op = rng.choice(("plan", "append", "attn", "attn", "attn"))
+    page = rng.choice((16, 32, 64, 128))
+    lens = rng.randrange(1, 1 << 20)
+    if op == "plan":
+        S = _log_int(rng, 1, 512)
+        most = _log_int(rng, 1, max(1, 32000 // S))
+        c = _case("", op, S, (0, _log_int(rng, 1, 32767)), (rng.randrange(2), most), page, pad=rng.randrange(40), lens=lens)
+    elif op == "append":
+        Hkv, d = rng.choice((1, 2, 3, 8)), rng.choice((64, 128))
+        S = _log_int(rng, 1, 64)
+        most = _log_int(rng, 1, max(1, 16384 // S))
+        c = _case("", op, S, (0, _log_int(rng, 1, 2047)), (rng.randrange(2), most), page, Hq=Hkv * rng.choice((1, 4)),
+                  Hkv=Hkv, d=d, dtype=rng.choice(("bf16", "bf16", "fp32")), pad=rng.randrange(40), lens=lens)
+    else:
+        d = rng.choice((64, 128, 128))
+        g = rng.choice((1, 2, 3, 4, 6, 8))
+        kind = rng.choice(("decode", "decode", "chunk", "mixed", "window", "fp32"))
+        Hkv = rng.choice((1, 2, 4, 8)) if g <= 4 else rng.choice((1, 2, 4))
+        Hq, dtype, window, chunks = g * Hkv, "bf16", 0, 0
+        if kind == "decode":
+            S = _log_int(rng, 1, 128)
+            new = (0 if S > 12 and rng.randrange(3) == 0 else 1, rng.choice((1, 1, 4)))
+            ctx = (0, _log_int(rng, 64, min(131071, (1 << 20) // S)))
+        elif kind == "chunk":
+            S = rng.choice((1, 1, 2))
+            most = _log_int(rng, 128, 4096 // S)
+            new, ctx = (max(1, most // 2), most), (0, _log_int(rng, 64, 16001))
+        elif kind == "mixed":
+            S = _log_int(rng, 4, 24)
+            chunks = rng.randrange(1, 4)
+            most = _log_int(rng, 16, 700)
+            new, ctx = (max(1, most // 4), most), (0, _log_int(rng, 16, 6000))
+        elif kind == "window":
+            S = rng.choice((1, 2, 3))
+            window = _log_int(rng, 8, 4096)
+            most = _log_int(rng, 64, 1500)
+            new, ctx = (max(1, most // 2), most), (0, _log_int(rng, 16, 9000))
+        else:
+            dtype = "fp32"
+            S = _log_int(rng, 1, 6)
+            new, ctx = (1, _log_int(rng, 4, 200)), (0, _log_int(rng, 16, 2000))
+        c = _case("", op, S, ctx, new, page, Hq=Hq, Hkv=Hkv, d=d, dtype=dtype, window=window, chunks=chunks,
+                  pad=rng.randrange(20), lens=lens)
+    del c["name"]
+    return c
+
+
+def lengths(case):
+    """(ctx, new) of the case's requests, int64 arrays."""
+    r = np.random.RandomState(case["lens"])
+    S, lo, hi = case["S"], case["ctx_lo"], case["ctx_hi"]
+    ctx = r.randint(lo, hi + 1, S).astype(np.int64)
+    new = r.randint(case["new_lo"], case["new_hi"] + 1, S).astype(np.int64)
+    if case["chunks"]:
+        keep = r.permutation(S) < case["chunks"]
+        new = np.where(keep, new, 1)
+    return ctx, new
+
+
+# ------------------------------------------------------------------ the inputs
+
+def prepare(case, seed):
+    ctx, new = lengths(case)
+    S, page, T = case["S"], case["page"], int(new.sum()) + case["pad"]
+    T = max(T, 1)
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(seed)
+    final = -(-(ctx + new) // page)                 # pages once the new tokens are in
+    before = -(-ctx // page)
+    width = int(final.max()) + 1
+    P = int(final.sum()) + 8
+    perm = torch.randperm(P, generator=gen, device=DEV).to(torch.int32)
+    # the step's plan starts from the pages of the cached tokens, the write and the attention from all of them
+    pages = before if case["op"] == "plan" else final
+    start = np.concatenate([[0], np.cumsum(pages)])
+    cell = np.arange(width)[None, :]
+    held_cells = cell < pages[:, None]
+    where_ = torch.from_numpy(np.where(held_cells, start[:-1, None] + cell, 0)).to(DEV)
+    held_mask = torch.from_numpy(held_cells).to(DEV)
+    table = torch.where(held_mask, perm[where_], torch.full_like(perm[:1], -1)).contiguous()
+    i32 = lambda a: torch.from_numpy(np.asarray(a)).to(device=DEV, dtype=torch.int32)  # noqa: E731
+    q_start = np.concatenate([[0], np.cumsum(new)])
+    st = {"op": case["op"], "page": page, "T": T, "S": S, "table": table, "q_start": i32(q_start),
+          "rows": int(new.sum()), "nmax": int(new.max()), "kvmax": int((ctx + new).max()), "window": case["window"]}
+    if case["op"] == "plan":
+        free = P - int(pages.sum())
+        ring = torch.full((P,), -1, device=DEV, dtype=torch.int32)
+        head = int(torch.randint(P, (1,), generator=gen, device=DEV))
+        ring[(head + torch.arange(free, device=DEV)) % P] = perm[P - free:]
+        st.update(ctx=i32(ctx), new=i32(new), none=i32(np.zeros(S)), held=i32(pages), ring=ring,
+                  free_state=i32([head, free]), kv_len=i32(np.zeros(S)),
+                  slots=torch.zeros(T, device=DEV, dtype=torch.int64),
+                  slots_back=torch.zeros(T, device=DEV, dtype=torch.int64),
+                  q_back=i32(np.zeros(S + 1)), kv_back=i32(np.zeros(S)))
+        st["q_start"] = i32(np.zeros(S + 1))
+        return st
+    Hq, Hkv, d, dt = case["Hq"], case["Hkv"], case["d"], TYPES[case["dtype"]]
+    # one projection's rows [T, (Hq + 2 Hkv) d], from which Q, K and V are views
+    qkv = torch.randn(T, Hq + 2 * Hkv, d, generator=gen, device=DEV, dtype=dt)
+    st.update(Q=qkv[:, :Hq], K=qkv[:, Hq:Hq + Hkv], V=qkv[:, Hq + Hkv:],
+              Kc=torch.randn(P, Hkv, page, d, generator=gen, device=DEV, dtype=dt),
+              Vc=torch.randn(P, Hkv, page, d, generator=gen, device=DEV, dtype=dt))
+    if case["op"] == "append":
+        pos = np.concatenate([np.arange(c, c + n) for c, n in zip(ctx, new)] + [np.zeros(0, dtype=np.int64)])
+        of = np.repeat(np.arange(S), new)
+        pos, of = torch.from_numpy(pos).to(DEV), torch.from_numpy(of).to(DEV)
+        slots = torch.full((T,), -1, device=DEV, dtype=torch.int64)
+        slots[:pos.numel()] = table[of, pos // page].long() * page + pos % page
+        st["slots"] = slots
+    else:
+        st.update(kv_len=i32(ctx + new), scale=1.0 / math.sqrt(d), out=torch.zeros(T, Hq, d, device=DEV, dtype=dt))
+    return st
+
+
+# ------------------------------------------------------------------ plain forms
+
+def _plan_plain(ctx, new, held, table, ring, free_state, T, page):
+    S, width = table.shape
+    P, dev = ring.shape[0], table.device
+    ctx, new, old = ctx.long(), new.long(), held.long()
+    rows = new.clamp(min=0)
+    q_end = rows.cumsum(0)
+    want = (ctx + new + page - 1) // page
+    fine = (ctx >= 0) & (new >= 0) & (want <= width) & (q_end <= T)
+    need = torch.where(fine, want - old, 0)
+    take, give = need.clamp(min=0), (-need).clamp(min=0)
+    take_end = take.cumsum(0)
+    head, count = free_state[0].long(), free_state[1].long()
+    served = fine & ((take == 0) | (take_end <= count))
+    take = torch.where(served, take, 0)
+    take_start, give_start = take.cumsum(0) - take, give.cumsum(0) - give
+    cell = torch.arange(width, device=dev)[None, :]
+    taken = (cell >= old[:, None]) & (cell < (old + take)[:, None])
+    given = (cell >= (old - give)[:, None]) & (cell < old[:, None])
+    from_ring = ring[(head + take_start[:, None] + cell - old[:, None]) % P]
+    to_ring = torch.where(given, (head + count + give_start[:, None] + cell - (old - give)[:, None]) % P, P)
+    more = torch.cat([ring, ring[:1]])
+    more[to_ring.reshape(-1)] = table.reshape(-1)
+    ring.copy_(more[:P])
+    table.copy_(torch.where(taken, from_ring, torch.where(given, -1, table)))
+    held.copy_(torch.where(served, want, old))
+    free_state.copy_(torch.stack([(head + take.sum()) % P, count - take.sum() + give.sum()]))
+    q_start = torch.cat([torch.zeros_like(q_end[:1]), q_end]).clamp(max=T).int()
+    kv_len = torch.where(served, ctx + new, 0).int()
+    t = torch.arange(T, device=dev)
+    s = torch.searchsorted(q_end, t, right=True)
+    live = s < S
+    s = s.clamp(max=S - 1)
+    pos = ctx[s] + t - (q_end[s] - rows[s])
+    live &= served[s]
+    page_id = table[s, (pos // page).clamp(0, width - 1)].long()
+    slots = torch.where(live, page_id * page + pos % page, -1)
+    return q_start, kv_len, slots
+
+
+def _append_plain(K, V, slots, Kc, Vc):
+    P, H, page, d = Kc.shape
+    live = (slots >= 0) & (slots < P * page)
+    at = torch.where(live, slots, 0)
+    # a row without a slot writes back what is there at slot 0's place, or what the row of slot 0 writes there
+    first = (slots == 0).to(torch.int32)
+    row0, has0 = first.argmax(), first.max() > 0
+    for rows, cache in ((K, Kc), (V, Vc)):
+        there = torch.where(has0, rows[row0], cache[0, :, 0])
+        cache[at // page, :, at % page] = torch.where(live[:, None, None], rows, there)
+
+
+def _attn_plain(Q, Kc, Vc, table, q_start, kv_len, scale, window, out, nmax, kvmax):
+    T, Hq, d = Q.shape
+    P, Hkv, page, _ = Kc.shape
+    S, g = kv_len.shape[0], Hq // Hkv
+    dev = Q.device
+    npages = -(-kvmax // page)
+    L = npages * page
+    full = torch.cat([out, out[:1]])                  # row T takes what belongs to no request
+    # as many requests at once as keep the score matrix within 12 GB
+    group = max(1, int(3e9 // max(1, Hq * nmax * L)))
+    key = torch.arange(L, device=dev)
+    for a in range(0, S, group):
+        b = min(S, a + group)
+        tab = table[a:b, :npages].clamp(0, P - 1).long()
+        k = Kc[tab].float().permute(0, 2, 1, 3, 4).reshape(b - a, Hkv, L, d)
+        v = Vc[tab].float().permute(0, 2, 1, 3, 4).reshape(b - a, Hkv, L, d)
+        n = (q_start[a + 1:b + 1] - q_start[a:b]).long()
+        i = torch.arange(nmax, device=dev)[None, :]
+        row = q_start[a:b].long()[:, None] + i
+        row = torch.where(i < n[:, None], row, T)
+        q = Q[row.clamp(max=T - 1)].float().reshape(b - a, nmax, Hkv, g, d).permute(0, 2, 1, 3, 4)
+        q = q.reshape(b - a, Hkv, nmax * g, d)
+        pos = (kv_len[a:b].long() - n)[:, None] + i
+        seen = key[None, None, :] <= pos[:, :, None]
+        if window > 0:
+            seen &= key[None, None, :] > pos[:, :, None] - window
+        v = torch.where((key[None, :] < kv_len[a:b, None])[:, None, :, None], v, 0.0)
+        s = (q @ k.transpose(-1, -2)).mul_(scale).reshape(b - a, Hkv, nmax, g, L)
+        s.masked_fill_(~seen[:, None, :, None, :], -math.inf)
+        m = s.amax(-1, keepdim=True)
+        p = s.sub_(torch.where(m == -math.inf, 0.0, m)).exp_()
+        l = p.sum(-1, keepdim=True).reshape(b - a, Hkv, nmax * g, 1)
+        o = (p.reshape(b - a, Hkv, nmax * g, L) @ v) / torch.where(l > 0, l, 1.0)
+        o = o.reshape(b - a, Hkv, nmax, g, d).permute(0, 2, 1, 3, 4).reshape(-1, Hq, d)
+        full[row.reshape(-1)] = o.to(out.dtype)
+    return full[:T]
+
+
+# ------------------------------------------------------------------ one pass
+
+def run(st):
+    if own:
+        from block_sparse_approximate_b200 import binding as bd
+    if st["op"] == "plan":
+        # a speculative step: pages and slots for the new tokens, then the same requests without them,
+        # which hands the pages back, so that the next pass finds the same lengths
+        if own:
+            bd.paged_plan(st["ctx"], st["new"], st["held"], st["table"], st["ring"], st["free_state"], st["T"],
+                          st["page"], q_start=st["q_start"], kv_len=st["kv_len"], slots=st["slots"])
+            bd.paged_plan(st["ctx"], st["none"], st["held"], st["table"], st["ring"], st["free_state"], st["T"],
+                          st["page"], q_start=st["q_back"], kv_len=st["kv_back"], slots=st["slots_back"])
+            names = ("q_start", "kv_len", "slots", "q_back", "kv_back", "slots_back", "held", "table", "ring",
+                     "free_state")
+            return [st[n] for n in names]
+        args = (st["held"], st["table"], st["ring"], st["free_state"], st["T"], st["page"])
+        grown = _plan_plain(st["ctx"], st["new"], *args)
+        back = _plan_plain(st["ctx"], st["none"], *args)
+        return [*grown, *back, st["held"], st["table"], st["ring"], st["free_state"]]
+    if st["op"] == "append":
+        if own:
+            bd.paged_append(st["K"], st["V"], st["slots"], st["Kc"], st["Vc"])
+        else:
+            _append_plain(st["K"], st["V"], st["slots"], st["Kc"], st["Vc"])
+        return [st["Kc"], st["Vc"]]
+    if own:
+        return bd.paged_attn_fwd(st["Q"], st["Kc"], st["Vc"], st["table"], st["q_start"], st["kv_len"], st["scale"],
+                                 window=st["window"], out=st["out"])
+    return _attn_plain(st["Q"], st["Kc"], st["Vc"], st["table"], st["q_start"], st["kv_len"], st["scale"],
+                       st["window"], st["out"], st["nmax"], st["kvmax"])
+
+
+# ------------------------------------------------------------------ what a pass cannot do without
+
+def work(case):
+    ctx, new = lengths(case)
+    page, rows = case["page"], int(new.sum())
+    T, S = max(1, rows + case["pad"]), case["S"]
+    if case["op"] == "plan":
+        final, before = -(-(ctx + new) // page), -(-ctx // page)
+        moved = int((final - before).sum())
+        looked = int(np.where(new > 0, -(-(ctx + new) // page) - ctx // page, 0).sum())
+        # each of the two calls: the three lengths in, q_start, kv_len and held out, 8 bytes a row of slots
+        each = S * 12 + S * 12 + 4 + 16 + 8 * T
+        return {"bytes": 2 * each + 4 * looked + 2 * 8 * moved + 4 * moved, "flops": 2 * (3 * S + 2 * T)}
+    e = 2 if case["dtype"] == "bf16" else 4
+    if case["op"] == "append":
+        return {"bytes": 4 * rows * case["Hkv"] * case["d"] * e + 8 * T, "flops": 0}
+    w = case["window"]
+    pairs = keys = 0
+    for c, n in zip(ctx.tolist(), new.tolist()):
+        if n == 0:
+            continue
+        pos = np.arange(c, c + n, dtype=np.int64)
+        pairs += int((np.minimum(pos + 1, w) if w else pos + 1).sum())
+        keys += c + n - (max(0, c - w + 1) if w else 0)
+    Hq, Hkv, d = case["Hq"], case["Hkv"], case["d"]
+    return {"bytes": 2 * rows * Hq * d * e + 2 * keys * Hkv * d * e + 4 * (keys // page + 2 * S),
+            "flops": 4 * Hq * d * pairs}
+
+
+# ------------------------------------------------------------------ the definition in 64 bits
+
+def _plan_exact(ctx, new, held, table, ring, free_state, T, page):
+    """The plan request by request, on the host, with Python's whole numbers."""
+    S, width, P = len(ctx), len(table[0]), len(ring)
+    head, count = free_state
+    q_start, kv_len, slots = [0], [0] * S, [-1] * T
+    taken, given, asked = 0, [], 0
+    for s in range(S):
+        first = q_start[-1]
+        end = first + max(0, new[s])
+        q_start.append(end)
+        want = -(-(ctx[s] + new[s]) // page)
+        if ctx[s] < 0 or new[s] < 0 or want > width or end > T:
+            continue
+        if want > held[s]:
+            asked += want - held[s]
+            if asked > count:
+                continue
+            for c in range(held[s], want):
+                table[s][c] = ring[(head + taken) % P]
+                taken += 1
+        for c in range(want, held[s]):
+            given.append(table[s][c])
+            table[s][c] = -1
+        held[s] = want
+        kv_len[s] = ctx[s] + new[s]
+        for i in range(new[s]):
+            at = ctx[s] + i
+            slots[first + i] = table[s][at // page] * page + at % page
+    for k, x in enumerate(given):
+        ring[(head + count + k) % P] = x
+    return [min(x, T) for x in q_start], kv_len, slots, held, table, ring, [(head + taken) % P, count - taken + len(given)]
+
+
+def exact(case, seed):
+    st = prepare(case, seed)
+    if st["op"] == "plan":
+        if st["S"] * st["table"].shape[1] > 4_000_000:
+            return None
+        state = [st[n].tolist() for n in ("held", "table", "ring", "free_state")]
+        a = _plan_exact(st["ctx"].tolist(), st["new"].tolist(), *state, st["T"], st["page"])
+        b = _plan_exact(st["ctx"].tolist(), st["none"].tolist(), *a[3:], st["T"], st["page"])
+        i32, i64 = torch.int32, torch.int64
+        kinds = (i32, i32, i64, i32, i32, i64, i32, i32, i32, i32)
+        return [torch.tensor(v, dtype=k) for v, k in zip((*a[:3], *b[:3], *b[3:]), kinds)]
+    page = st["page"]
+    if st["op"] == "append":
+        found = []
+        for rows, cache in ((st["K"], st["Kc"]), (st["V"], st["Vc"])):
+            c = cache.double()
+            slots = st["slots"].cpu()
+            t = torch.nonzero(slots >= 0).flatten()
+            at = slots[t].to(DEV)
+            flat = c.transpose(1, 2).reshape(-1, c.shape[1], c.shape[3])
+            flat[at] = rows.double()[t.to(DEV)]
+            found.append(flat.reshape(c.shape[0], page, c.shape[1], c.shape[3]).transpose(1, 2).contiguous())
+        return found
+    ctx, new = lengths(case)
+    Hkv = case["Hkv"]
+    g = case["Hq"] // Hkv
+    out = st["out"].double()
+    first = 0
+    for s, (c, n) in enumerate(zip(ctx.tolist(), new.tolist())):
+        if n == 0:
+            continue
+        kv = c + n
+        ids = st["table"][s, : -(-kv // page)].long()
+        pos = torch.arange(c, kv, device=DEV)
+        key = torch.arange(kv, device=DEV)
+        seen = key[None, :] <= pos[:, None]
+        if case["window"]:
+            seen &= key[None, :] > pos[:, None] - case["window"]
+        for h in range(Hkv):
+            k = st["Kc"][ids, h].reshape(-1, case["d"])[:kv].double()
+            v = st["Vc"][ids, h].reshape(-1, case["d"])[:kv].double()
+            for j in range(h * g, h * g + g):
+                q = st["Q"][first:first + n, j].double()
+                z = torch.einsum("nd,kd->nk", q, k) * st["scale"]
+                z = torch.where(seen, z, torch.tensor(-math.inf, device=DEV, dtype=torch.float64))
+                out[first:first + n, j] = torch.softmax(z, dim=-1) @ v
+        first += n
+    return out
