@@ -182,7 +182,7 @@ def _plan_plain(ctx, new, held, table, ring, free_state, T, page):
     rows = new.clamp(min=0)
     q_end = rows.cumsum(0)
     want = (ctx + new + page - 1) // page
-    fine = (ctx >= 0) & (new >= 0) & (want <= width) & (q_end <= T)
+    fine = (ctx >= 0) & (new >= 0) & (want <= width) & ((new == 0) | (q_end <= T))
     need = torch.where(fine, want - old, 0)
     take, give = need.clamp(min=0), (-need).clamp(min=0)
     take_end = take.cumsum(0)
@@ -339,7 +339,7 @@ def _plan_exact(ctx, new, held, table, ring, free_state, T, page):
         end = first + max(0, new[s])
         q_start.append(end)
         want = -(-(ctx[s] + new[s]) // page)
-        if ctx[s] < 0 or new[s] < 0 or want > width or end > T:
+        if ctx[s] < 0 or new[s] < 0 or want > width or (new[s] > 0 and end > T):
             continue
         if want > held[s]:
             asked += want - held[s]
