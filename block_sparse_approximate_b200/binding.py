@@ -30,6 +30,7 @@ EXPORTS = ("sa_block_pool", "sa_route", "sa_sparse_attn_fwd", "sa_decode_workspa
            "sa_sfa_encode", "sa_sfa_densify", "sa_sfa_workspace_size", "sa_sfa_attn_fwd",
            "sa_sparse_attn_bwd_workspace_size", "sa_sparse_attn_bwd", "sa_sparse_attn_fwd_lse",
            "sa_sparse_attn_bwd_lse", "sa_sparse_attn_bwd_linear_mix_workspace_size", "sa_sparse_attn_bwd_linear_mix",
+           "sa_paged_plan", "sa_paged_append", "sa_paged_attn_workspace_size", "sa_paged_attn_fwd",
            "sa_device_error", "sa_last_error", "sa_version")
 
 
@@ -47,6 +48,11 @@ class Shape(ctypes.Structure):
 class DecodeShape(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int32), ("Hq", ctypes.c_int32), ("Hkv", ctypes.c_int32),
                 ("N", ctypes.c_int32), ("d", ctypes.c_int32), ("block", ctypes.c_int32)]
+
+
+class PagedShape(ctypes.Structure):
+    _fields_ = [("S", ctypes.c_int32), ("T", ctypes.c_int32), ("Hq", ctypes.c_int32), ("Hkv", ctypes.c_int32),
+                ("d", ctypes.c_int32), ("page", ctypes.c_int32), ("P", ctypes.c_int32), ("max_pages", ctypes.c_int32)]
 
 
 _STAT_FIELDS = ("qmean", "kmean", "vsum", "kvar", "zrelu", "htot", "ztot", "kmean_bf16", "vmean_bf16",
@@ -107,7 +113,13 @@ def load():
     lib.sa_sparse_attn_bwd_linear_mix_workspace_size.restype = sz
     lib.sa_sparse_attn_bwd_linear_mix.argtypes = [vp, vp, vp, vp, vp, ctypes.c_int, Shape, vp, i32, vp,
                                                   ctypes.POINTER(BlockStats), f32, vp, vp, vp, vp, sz, vp]
-    for fn in ("sa_block_pool", "sa_route", "sa_sparse_attn_fwd", "sa_decode_fwd", "sa_decode_fwd_static",
+    lib.sa_paged_plan.argtypes = [vp, vp, PagedShape, vp, vp, vp, vp, vp, vp, vp, vp]
+    lib.sa_paged_append.argtypes = [vp, vp, i64, i64, ctypes.c_int, PagedShape, vp, vp, vp, vp]
+    lib.sa_paged_attn_workspace_size.argtypes = [PagedShape]
+    lib.sa_paged_attn_workspace_size.restype = sz
+    lib.sa_paged_attn_fwd.argtypes = [vp, i64, vp, vp, ctypes.c_int, PagedShape, vp, vp, vp, i32, f32, vp, vp, sz, vp]
+    for fn in ("sa_paged_plan", "sa_paged_append", "sa_paged_attn_fwd",
+               "sa_block_pool", "sa_route", "sa_sparse_attn_fwd", "sa_decode_fwd", "sa_decode_fwd_static",
                "sa_quantize_e4m3", "sa_sparse_attn_fwd_fp8", "sa_sfa_encode", "sa_sfa_densify", "sa_sfa_attn_fwd",
                "sa_sparse_attn_bwd", "sa_sparse_attn_fwd_lse", "sa_sparse_attn_bwd_lse",
                "sa_sparse_attn_bwd_linear_mix"):
@@ -428,3 +440,131 @@ def sparse_attn_bwd_linear_mix(Q, K, V, O, dO, block_idx, block: int, alpha, sta
                                              ctypes.byref(cst), float(scale), _ptr(dQ), _ptr(dK), _ptr(dV),
                                              _ptr(workspace), workspace.numel(), _stream(stream)))
     return dQ, dK, dV
+
+
+# ---------------------------------------------------------------- paged KV cache
+
+def _paged_ptrs(dev, dtypes, names, tensors, contiguous=True):
+    """Pointers of tensors that must live on ``dev`` with the given dtypes."""
+    ptrs = []
+    for t, dt, n in zip(tensors, dtypes, names):
+        if t.device != dev or dev.type != "cuda":
+            raise ValueError(f"{n} must live on the call's CUDA device")
+        if t.dtype != dt:
+            raise ValueError(f"{n} must be {dt}, not {t.dtype}")
+        if contiguous and not t.is_contiguous():
+            raise ValueError(f"{n} must be contiguous")
+        ptrs.append(t.data_ptr())
+    return ptrs
+
+
+def _paged_rows(t: torch.Tensor, name: str) -> int:
+    """The row stride (elements) of packed rows [T, heads, d] whose rows are dense."""
+    T, H, d = t.shape
+    s0, s1, s2 = t.stride()
+    if t.numel() and ((d > 1 and s2 != 1) or (H > 1 and s1 != d)):
+        raise ValueError(f"{name}: the heads of a row must be contiguous (only the row stride is free)")
+    return s0 if T > 1 else H * d
+
+
+def _paged_run(dev, stream, fn: str, *args):
+    """Calls the C entry point with ``dev`` current, on ``stream`` (default: the device's current stream)."""
+    s = (stream if stream is not None else torch.cuda.current_stream(dev)).cuda_stream
+    f = getattr(load(), fn)
+    if dev.index == torch.cuda.current_device():
+        status = f(*args, s)
+    else:
+        with torch.cuda.device(dev):
+            status = f(*args, s)
+    if status != SA_OK:
+        _check(fn, status)
+
+
+def _paged_empty(shape, dev, dtype, stream):
+    """torch.empty on the stream that will use it, so that the caching allocator's reuse stays ordered with it."""
+    if stream is None:
+        return torch.empty(shape, device=dev, dtype=dtype)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, device=dev, dtype=dtype)
+
+
+def paged_plan(ctx_len: torch.Tensor, new_len: torch.Tensor, held: torch.Tensor, table: torch.Tensor,
+               free_pages: torch.Tensor, free_state: torch.Tensor, tokens: int, page: int, *, q_start=None,
+               kv_len=None, slots=None, stream=None):
+    """Pages and places of a serving step's new tokens, from the requests'
+    lengths (int32 [S]): updates held [S], table [S,max_pages], free_pages [P]
+    and free_state [2] (all int32) in place and returns (q_start int32 [S+1],
+    kv_len int32 [S], slots int64 [tokens]).  ``tokens``: rows of the step's
+    packed arrays, padding included.  See sa_paged_plan for refused requests."""
+    dev = ctx_len.device
+    S, i32 = ctx_len.shape[0], torch.int32
+    if table.dim() != 2 or table.shape[0] != S or new_len.shape != (S,) or held.shape != (S,):
+        raise ValueError("new_len and held must be [S], table [S, max_pages]")
+    if free_state.shape != (2,) or free_pages.dim() != 1:
+        raise ValueError("free_state must be [2], free_pages [P]")
+    if q_start is None:
+        q_start = _paged_empty((S + 1,), dev, i32, stream)
+    if kv_len is None:
+        kv_len = _paged_empty((S,), dev, i32, stream)
+    if slots is None:
+        slots = _paged_empty((tokens,), dev, torch.int64, stream)
+    if q_start.shape != (S + 1,) or kv_len.shape != (S,) or slots.shape != (tokens,):
+        raise ValueError("q_start must be [S + 1], kv_len [S], slots [tokens]")
+    ptrs = _paged_ptrs(dev, (i32,) * 8 + (torch.int64,),
+                       ("ctx_len", "new_len", "held", "table", "free_pages", "free_state", "q_start", "kv_len", "slots"),
+                       (ctx_len, new_len, held, table, free_pages, free_state, q_start, kv_len, slots))
+    shape = PagedShape(S, tokens, 1, 1, 64, page, free_pages.shape[0], table.shape[1])
+    _paged_run(dev, stream, "sa_paged_plan", ptrs[0], ptrs[1], shape, *ptrs[2:])
+    return q_start, kv_len, slots
+
+
+def paged_append(K: torch.Tensor, V: torch.Tensor, slots: torch.Tensor, Kcache: torch.Tensor, Vcache: torch.Tensor, *,
+                 stream=None) -> None:
+    """Writes the rows K, V [T,Hkv,d] (views with a row stride serve) to their
+    slots (int64 [T], negative: skipped) in the pools [P,Hkv,page,d]."""
+    dev, dt = Kcache.device, Kcache.dtype
+    P, Hkv, page, d = Kcache.shape
+    T = K.shape[0]
+    if Vcache.shape != Kcache.shape or K.shape != (T, Hkv, d) or V.shape != (T, Hkv, d) or slots.shape != (T,):
+        raise ValueError("K and V must be [T,Hkv,d], slots [T], the caches [P,Hkv,page,d]")
+    k, v = _paged_ptrs(dev, (dt, dt), ("K", "V"), (K, V), contiguous=False)
+    sl, kc, vc = _paged_ptrs(dev, (torch.int64, dt, dt), ("slots", "Kcache", "Vcache"), (slots, Kcache, Vcache))
+    _paged_run(dev, stream, "sa_paged_append", k, v, _paged_rows(K, "K"), _paged_rows(V, "V"), _dtype_code(Kcache),
+               PagedShape(0, T, Hkv, Hkv, d, page, P, 0), sl, kc, vc)
+
+
+def paged_attn_workspace_size(S: int, T: int, Hq: int, Hkv: int, d: int, page: int, P: int, max_pages: int) -> int:
+    return int(load().sa_paged_attn_workspace_size(PagedShape(S, T, Hq, Hkv, d, page, P, max_pages)))
+
+
+def paged_attn_fwd(Q: torch.Tensor, Kcache: torch.Tensor, Vcache: torch.Tensor, table: torch.Tensor,
+                   q_start: torch.Tensor, kv_len: torch.Tensor, scale: float, *, window: int = 0, out=None,
+                   workspace=None, stream=None) -> torch.Tensor:
+    """Causal (and, with ``window`` > 0, sliding-window) attention of the packed
+    rows Q [T,Hq,d] over their requests' pages; returns O [T,Hq,d], in which
+    the rows from q_start[S] on are not written.  Chunks of prompts and
+    single decoded tokens may share a call."""
+    dev, dt = Q.device, Q.dtype
+    T, Hq, d = Q.shape
+    P, Hkv, page, dc = Kcache.shape
+    S = kv_len.shape[0]
+    if Vcache.shape != Kcache.shape or dc != d:
+        raise ValueError("the caches must be [P,Hkv,page,d] with Q's d")
+    if table.dim() != 2 or table.shape[0] != S or q_start.shape != (S + 1,):
+        raise ValueError("q_start must be [S + 1], kv_len [S], table [S, max_pages]")
+    if out is None:
+        out = _paged_empty((T, Hq, d), dev, dt, stream)
+    elif out.shape != Q.shape:
+        raise ValueError("out must have Q's shape")
+    shape = PagedShape(S, T, Hq, Hkv, d, page, P, table.shape[1])
+    if workspace is None:
+        need = int(load().sa_paged_attn_workspace_size(shape))
+        workspace = _paged_empty((max(need, 256),), dev, torch.uint8, stream)
+    (q,) = _paged_ptrs(dev, (dt,), ("Q",), (Q,), contiguous=False)
+    kc, vc, tab, qs, kl, o, ws = _paged_ptrs(
+        dev, (dt, dt, torch.int32, torch.int32, torch.int32, dt, torch.uint8),
+        ("Kcache", "Vcache", "table", "q_start", "kv_len", "out", "workspace"),
+        (Kcache, Vcache, table, q_start, kv_len, out, workspace))
+    _paged_run(dev, stream, "sa_paged_attn_fwd", q, _paged_rows(Q, "Q"), kc, vc, _dtype_code(Q), shape, qs, kl, tab,
+               int(window), float(scale), o, ws, workspace.numel())
+    return out

@@ -1,0 +1,237 @@
+// Paged KV cache: what the plan, the append and the attention kernels share.
+//
+// The cache is a pool of P pages, [P][Hkv][page][d] for K and for V; request s
+// owns the pages table[s][0 .. ceil(len / page)).  The rows of all requests'
+// new tokens are packed one behind the other; request s has the rows
+// q_start[s] .. q_start[s+1].
+//
+// Work division of the attention.  The query rows of one (request, KV head)
+// are numbered token-major, r = token * group + (query head within the
+// group), so that a tile of BM consecutive rows shares its keys.  An item is
+// such a tile; its keys are the span its rows can see, walked in tiles of BN
+// keys.  The items of all requests are laid on one line, each as long as its
+// cost, and the line is cut into equal shares, one per CTA: a share starts
+// and ends anywhere, also inside an item.  A CTA that holds all key tiles of
+// an item writes its output; otherwise each CTA writes a partial state
+// (unnormalised sums, row maxima and sums) and paged_combine_kernel merges
+// them in key order.  Every CTA derives the line from q_start and kv_len by
+// itself, so no lengths are read by the host and a captured graph follows
+// them.
+#pragma once
+
+#include "common.cuh"
+
+namespace sa {
+namespace paged {
+
+constexpr int kMaxRequests = 4096;
+
+struct Params {
+  const int32_t* q_start;   // [S+1]
+  const int32_t* kv_len;    // [S]
+  const int32_t* table;     // [S][max_pages]
+  int S, T, Hq, Hkv, group, page_shift, P, max_pages;
+  int window;               // 0: none; else below max_pages * page
+};
+
+// Partial states in the workspace: slot 2c holds the first item portion of
+// CTA c, slot 2c + 1 the last one.  desc[c] describes the split item whose
+// first key tile lies with CTA c.
+struct Desc {
+  int64_t start, total;     // the item's place on the line, the line's length
+  int32_t parts;            // shares of the line
+  int32_t valid, slot, unit, nt, row0, r0, rv, h, pad;
+};
+
+struct Workspace {
+  Desc* desc;               // [ctas]
+  float* o;                 // [2 ctas][rows_cap][d]
+  float* ml;                // [2 ctas][rows_cap][2]: running maximum (log2 units), sum
+  int rows_cap, ctas;
+};
+
+// ---- the items of a request
+struct Request {
+  int row0, n, len;
+};
+
+__device__ __forceinline__ Request load_request(const Params& p, int s) {
+  // lengths come from device memory: bounded here, so that no table or row
+  // access can leave its array whatever they hold
+  const int a = min(max(p.q_start[s], 0), p.T);
+  const int b = min(max(p.q_start[s + 1], a), p.T);
+  return {a, b - a, min(max(p.kv_len[s], 0), p.max_pages << p.page_shift)};
+}
+
+struct Item {
+  int r0, rv;        // first row within the request, number of rows
+  int p0;            // position of the request's first new token (negative: rows before it see no key)
+  int lo, hi;        // keys that some row sees
+  int t0, nt;        // their tiles
+  int unit;          // cost of a tile
+};
+
+// A tiling is {BM rows, BN keys; up to kHalf rows cost kUnitHalf per tile
+// instead of kUnit; kOver is an item's own cost in the same unit; a share
+// holds at least kMinShare}.
+template <class TL>
+__device__ __forceinline__ Item item_of(const Request& q, int group, int window, int j) {
+  Item it;
+  it.r0 = j * TL::BM;
+  it.rv = min(TL::BM, q.n * group - it.r0);
+  it.p0 = q.len - q.n;
+  const int p_lo = it.p0 + it.r0 / group, p_hi = it.p0 + (it.r0 + it.rv - 1) / group;
+  it.lo = window > 0 ? max(0, p_lo - window + 1) : 0;
+  it.hi = max(0, p_hi + 1);
+  it.t0 = it.lo / TL::BN;
+  it.nt = it.hi > it.lo ? (it.hi + TL::BN - 1) / TL::BN - it.t0 : 0;
+  it.unit = it.rv <= TL::kHalf ? TL::kUnitHalf : TL::kUnit;
+  return it;
+}
+template <class TL>
+__device__ __forceinline__ int item_cost(const Item& it) { return it.nt * it.unit + TL::kOver; }
+template <class TL>
+__device__ __forceinline__ int items_of(const Request& q, int group) { return (q.n * group + TL::BM - 1) / TL::BM; }
+
+__device__ __forceinline__ int64_t share_start(int64_t total, int parts, int c) { return total * c / parts; }
+template <class TL>
+__device__ __forceinline__ int share_count(int64_t total, int ctas) {
+  const int64_t n = total / TL::kMinShare;
+  return (int)(n < 1 ? 1 : (n < ctas ? n : ctas));
+}
+
+// Lays the line: pre[s] = the end of request s on it (all threads of a block
+// of kThreads; pre and tot in shared memory).  Returns the line's length.
+template <class TL, int kThreads>
+__device__ int64_t lay_line(const Params& p, int64_t* pre, int64_t* tot) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t run = 0;
+  for (int base = 0; base < p.S; base += kThreads) {
+    const int s = base + threadIdx.x;
+    Request q{0, 0, 0};
+    if (s < p.S) q = load_request(p, s);
+    const int nj = items_of<TL>(q, p.group);
+    int64_t c = 0;
+    if (nj <= 2)
+      for (int j = 0; j < nj; ++j) c += item_cost<TL>(item_of<TL>(q, p.group, p.window, j));
+    // requests of many items: the warp takes them one by one, a lane an item
+    for (unsigned big = __ballot_sync(0xffffffffu, nj > 2); big; big &= big - 1) {
+      const int src = __ffs(big) - 1;
+      const Request b{0, __shfl_sync(0xffffffffu, q.n, src), __shfl_sync(0xffffffffu, q.len, src)};
+      const int nb = items_of<TL>(b, p.group);
+      int64_t sum = 0;
+      for (int j = lane; j < nb; j += 32) sum += item_cost<TL>(item_of<TL>(b, p.group, p.window, j));
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      if (lane == src) c = sum;
+    }
+    c *= p.Hkv;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, c, o);
+      if (lane >= o) c += y;
+    }
+    if (lane == 31) tot[warp] = c;
+    __syncthreads();
+    int64_t off = run, all = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) off += tot[w];
+      all += tot[w];
+    }
+    if (s < p.S) pre[s] = off + c;
+    run += all;
+    __syncthreads();
+  }
+  return run;
+}
+
+// One warp walks the items of a share.
+template <class TL>
+struct Walker {
+  Request q;
+  Item it;
+  int s, h, j, nj, cost;
+  int64_t start;
+
+  __device__ __forceinline__ void set_item(const Params& p) {
+    it = item_of<TL>(q, p.group, p.window, j);
+    cost = item_cost<TL>(it);
+  }
+  // The item that holds place w of the line, 0 <= w < its length.
+  __device__ void find(const Params& p, const int64_t* pre, int64_t w) {
+    const int lane = threadIdx.x & 31;
+    int a = 0, b = p.S - 1;
+    while (a < b) {
+      const int m = (a + b) >> 1;
+      if (pre[m] > w) b = m;
+      else a = m + 1;
+    }
+    s = a;
+    const int64_t first = s ? pre[s - 1] : 0;
+    const int64_t head = (pre[s] - first) / p.Hkv;
+    h = (int)((w - first) / head);
+    int64_t at = first + h * head;
+    q = load_request(p, s);
+    nj = items_of<TL>(q, p.group);
+    for (j = 0;; j += 32) {
+      const int mine = j + lane < nj ? item_cost<TL>(item_of<TL>(q, p.group, p.window, j + lane)) : 0;
+      int64_t end = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, end, o);
+        if (lane >= o) end += y;
+      }
+      const unsigned past = __ballot_sync(0xffffffffu, at + end > w);
+      if (past) {
+        const int src = __ffs(past) - 1;
+        start = at + __shfl_sync(0xffffffffu, end - mine, src);
+        j += src;
+        break;
+      }
+      at += __shfl_sync(0xffffffffu, end, 31);
+      if (j + 32 >= nj) {   // not reached while the line is the sum of its items
+        j = nj - 1;
+        start = at;
+        break;
+      }
+    }
+    set_item(p);
+  }
+  __device__ __forceinline__ bool next(const Params& p) {
+    start += cost;
+    if (++j == nj) {
+      j = 0;
+      if (++h == p.Hkv) {
+        h = 0;
+        do {
+          if (++s >= p.S) return false;
+          q = load_request(p, s);
+        } while (q.n == 0);
+        nj = items_of<TL>(q, p.group);
+      }
+    }
+    set_item(p);
+    return true;
+  }
+  // Key tiles [ta, tb) of the item in the share [w0, w1); false: none here.
+  __device__ __forceinline__ bool portion(int64_t w0, int64_t w1, int& ta, int& tb) const {
+    ta = w0 > start ? min(it.nt, (int)((w0 - start) / it.unit)) : 0;
+    tb = w1 - start >= cost ? it.nt : min(it.nt, (int)((w1 - start) / it.unit));
+    return it.nt == 0 ? start >= w0 : ta < tb;
+  }
+};
+
+// ---- host side
+struct Limits {
+  static constexpr int kCtas = 148;        // CTAs of the tensor-core kernel: one per SM
+  static constexpr int kCtasSimt = 296;    // CTAs of the CUDA-core kernel: two per SM
+};
+
+}  // namespace paged
+
+// The bf16 attention on the tensor cores (paged_attn_tc.cu).
+sa_status paged_attn_tc(const void* Q, int64_t q_stride, const void* Kc, const void* Vc, const sa_paged_shape& s,
+                        const paged::Params& p, float scale, void* O, const paged::Workspace& ws, cudaStream_t stream);
+uint32_t paged_tc_error_take();
+
+}  // namespace sa

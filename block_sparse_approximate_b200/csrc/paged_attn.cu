@@ -1,0 +1,478 @@
+// Attention of new tokens over a paged KV cache: the entry point, the
+// CUDA-core kernel for fp32 and the merge of split items.  The bf16 kernel is
+// in paged_attn_tc.cu.
+#include <algorithm>
+
+#include "paged.cuh"
+
+namespace sa {
+
+sa_status check_paged_heads(const sa_paged_shape& s, sa_dtype dtype, const char* fn);
+
+namespace {
+
+using namespace paged;
+
+// ---------------------------------------------------------------- CUDA-core kernel
+// Tiles of 64 rows and 64 keys, 256 threads, two CTAs per SM.  Thread (ty,
+// tx) holds scores of rows ty + 16 i and keys tx + 16 j (4 x 4) and outputs of
+// the same rows (d / 16 columns); a row's maximum and sum are reduced over
+// its 16 tx lanes, in 32 bits as the products are.  Bound by the FMA pipe for
+// prompts; items of up to 16 rows (decode) form only the row group i = 0.
+constexpr int kSimtThreads = 256;
+struct SimtTiling {
+  static constexpr int BM = 64, BN = 64;
+  // a tile of at most 16 rows costs its loads, about half a full tile
+  static constexpr int kHalf = 16, kUnit = 4, kUnitHalf = 2, kOver = 2, kMinShare = 4;
+};
+constexpr int kPitchP = 68;
+
+template <typename T>
+__device__ __forceinline__ float4 load4(const T* p);
+template <>
+__device__ __forceinline__ float4 load4<float>(const float* p) { return __ldg(reinterpret_cast<const float4*>(p)); }
+template <>
+__device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16* p) {
+  const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
+  const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.x));
+  const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.y));
+  return make_float4(a.x, a.y, b.x, b.y);
+}
+
+template <int D>
+constexpr size_t simt_smem() { return (size_t)(2 * 64 * (D + 4) + 64 * kPitchP) * 4; }
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kSimtThreads, 2)
+paged_attn_simt_kernel(const T* __restrict__ Q, int64_t q_stride, const T* __restrict__ Kc, const T* __restrict__ Vc,
+                       Params p, float scale2, T* __restrict__ O, Workspace ws) {
+  pdl_wait();
+  pdl_trigger();
+  using TL = SimtTiling;
+  constexpr int DP = D + 4, NC = D / 64;        // NC float4 columns of the output per thread
+  extern __shared__ __align__(16) float smem_f[];
+  float* sq = smem_f;
+  float* skv = sq + 64 * DP;
+  float* sp = skv + 64 * DP;
+  __shared__ int64_t tot[kSimtThreads / 32];
+  __shared__ int64_t share[2];
+  __shared__ int parts_s;
+  struct Job {
+    int live, s, h, row0, r0, rv, p0, lo, hi, t0, ta, tb, slot;   // slot < 0: the whole item
+  };
+  __shared__ Job job;
+  const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15, warp = tid >> 5, lane = tid & 31;
+  const int c = blockIdx.x;
+
+  // the line, laid in the operand buffers before their first use
+  int64_t* pre = reinterpret_cast<int64_t*>(smem_f);
+  const int64_t total = lay_line<TL, kSimtThreads>(p, pre, tot);
+  const int parts = share_count<TL>(total, ws.ctas);
+  if (tid == 0) {
+    ws.desc[c].valid = 0;
+    share[0] = share_start(total, parts, c);
+    share[1] = share_start(total, parts, c + 1);
+    parts_s = parts;
+  }
+  if (total == 0 || c >= parts) return;
+  Walker<TL> w;
+  __syncthreads();
+  const int64_t w0 = share[0], w1 = share[1];
+  bool more = true;
+  if (warp == 0) w.find(p, pre, w0);
+  __syncthreads();                              // the line is read; its memory becomes the operands'
+  int emitted = 0;
+  bool first = true;
+
+  for (;;) {
+    if (warp == 0) {
+      // the next portion of the share
+      int ta = 0, tb = 0;
+      bool got = false;
+      while (more && !got) {
+        if (!first) more = w.next(p);
+        first = false;
+        if (!more || w.start >= w1) {
+          more = false;
+          break;
+        }
+        got = w.portion(w0, w1, ta, tb);
+      }
+      if (lane == 0) {
+        job.live = got;
+        if (got) {
+          const bool whole = ta == 0 && tb == w.it.nt;
+          const int slot = whole ? -1 : 2 * c + (emitted > 0);
+          job = Job{1, w.s, w.h, w.q.row0, w.it.r0, w.it.rv, w.it.p0, w.it.lo, w.it.hi, w.it.t0, ta, tb, slot};
+          if (!whole && ta == 0)
+            ws.desc[c] = Desc{w.start, total, parts_s, 1, slot, w.it.unit, w.it.nt, w.q.row0, w.it.r0, w.it.rv, w.h, 0};
+        }
+      }
+      emitted += got;
+    }
+    __syncthreads();
+    const Job jb = job;
+    if (!jb.live) return;
+
+    // queries, scaled to log2 units
+    for (int x = tid; x < 64 * (D / 4); x += kSimtThreads) {
+      const int r = x / (D / 4), e = 4 * (x % (D / 4));
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (r < jb.rv) {
+        const int rr = jb.r0 + r;
+        v = load4(Q + (int64_t)(jb.row0 + rr / p.group) * q_stride + (int64_t)(jb.h * p.group + rr % p.group) * D + e);
+        v.x *= scale2; v.y *= scale2; v.z *= scale2; v.w *= scale2;
+      }
+      *reinterpret_cast<float4*>(sq + r * DP + e) = v;
+    }
+    float m[4], l[4], o[4][NC * 4];
+    int last[4];                                // the row's last visible key
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      m[i] = -INFINITY;
+      l[i] = 0.f;
+      const int r = ty + 16 * i;
+      last[i] = r < jb.rv ? jb.p0 + (jb.r0 + r) / p.group : -1;
+#pragma unroll
+      for (int k = 0; k < NC * 4; ++k) o[i][k] = 0.f;
+    }
+    const int mask = (1 << p.page_shift) - 1;
+    auto load_tile = [&](const T* cache, int k0) {
+      for (int x = tid; x < 64 * (D / 4); x += kSimtThreads) {
+        const int r = x / (D / 4), e = 4 * (x % (D / 4)), key = k0 + r;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (key >= jb.lo && key < jb.hi) {
+          const int id = p.table[(size_t)jb.s * p.max_pages + (key >> p.page_shift)];
+          if (id >= 0 && id < p.P)
+            v = load4(cache + ((((int64_t)id * p.Hkv + jb.h) << p.page_shift) + (key & mask)) * D + e);
+        }
+        *reinterpret_cast<float4*>(skv + r * DP + e) = v;
+      }
+    };
+    // one key tile; NI: row groups of 16 that hold rows
+    auto tile = [&](auto ni, int k0) {
+      constexpr int NI = decltype(ni)::value;
+      float s[NI][4];
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+#pragma unroll 8
+      for (int e = 0; e < D; e += 4) {
+        float4 a[NI], b[4];
+#pragma unroll
+        for (int i = 0; i < NI; ++i) a[i] = *reinterpret_cast<const float4*>(sq + (ty + 16 * i) * DP + e);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const float4*>(skv + (tx + 16 * j) * DP + e);
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            s[i][j] = fmaf(a[i].x, b[j].x, fmaf(a[i].y, b[j].y, fmaf(a[i].z, b[j].z, fmaf(a[i].w, b[j].w, s[i][j]))));
+      }
+      bool edge = false;                        // some row does not see the whole tile
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        float mx = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int key = k0 + tx + 16 * j;
+          const bool seen = key <= last[i] && (p.window == 0 || key > last[i] - p.window);
+          edge |= !seen;
+          s[i][j] = seen ? s[i][j] : -INFINITY;
+          mx = fmaxf(mx, s[i][j]);
+        }
+#pragma unroll
+        for (int d = 8; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+        const float mn = fmaxf(m[i], mx);
+        const float base = mn == -INFINITY ? 0.f : mn;     // no key yet: every term is 2^-inf = 0
+        const float f = fast_exp2(m[i] - base);
+        m[i] = mn;
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float e = fast_exp2(s[i][j] - base);
+          sum += e;
+          sp[(ty + 16 * i) * kPitchP + tx + 16 * j] = e;
+        }
+#pragma unroll
+        for (int d = 8; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        l[i] = l[i] * f + sum;
+#pragma unroll
+        for (int k = 0; k < NC * 4; ++k) o[i][k] *= f;
+      }
+      const bool guard = __syncthreads_or(edge);           // scores stored, K read
+      load_tile(Vc, k0);
+      __syncthreads();
+      auto product = [&](auto guarded) {
+#pragma unroll 4
+        for (int k = 0; k < 64; k += 4) {
+          float4 a[NI];
+#pragma unroll
+          for (int i = 0; i < NI; ++i) a[i] = *reinterpret_cast<const float4*>(sp + (ty + 16 * i) * kPitchP + k);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            float4 b[NC];
+#pragma unroll
+            for (int n = 0; n < NC; ++n) b[n] = *reinterpret_cast<const float4*>(skv + (k + kk) * DP + 4 * tx + 64 * n);
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+              const float e = kk == 0 ? a[i].x : kk == 1 ? a[i].y : kk == 2 ? a[i].z : a[i].w;
+              // a masked key's term is absent, also where its value is not finite
+              if (decltype(guarded)::value) {
+                const int key = k0 + k + kk;
+                if (key > last[i] || (p.window > 0 && key <= last[i] - p.window)) continue;
+              }
+#pragma unroll
+              for (int n = 0; n < NC; ++n) {
+                o[i][4 * n] = fmaf(e, b[n].x, o[i][4 * n]);
+                o[i][4 * n + 1] = fmaf(e, b[n].y, o[i][4 * n + 1]);
+                o[i][4 * n + 2] = fmaf(e, b[n].z, o[i][4 * n + 2]);
+                o[i][4 * n + 3] = fmaf(e, b[n].w, o[i][4 * n + 3]);
+              }
+            }
+          }
+        }
+      };
+      if (guard) product(std::true_type{});
+      else product(std::false_type{});
+    };
+    for (int t = jb.ta; t < jb.tb; ++t) {
+      const int k0 = (jb.t0 + t) * 64;
+      __syncthreads();                          // the previous tile's V is read
+      load_tile(Kc, k0);
+      __syncthreads();
+      if (jb.rv <= 16) tile(std::integral_constant<int, 1>{}, k0);
+      else tile(std::integral_constant<int, 4>{}, k0);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = ty + 16 * i;
+      if (r >= jb.rv) continue;
+      const int rr = jb.r0 + r;
+      if (jb.slot < 0) {
+        const float inv = l[i] > 0.f ? 1.0f / l[i] : (l[i] == 0.f ? 0.f : l[i]);
+        T* dst = O + ((int64_t)(jb.row0 + rr / p.group) * p.Hq + jb.h * p.group + rr % p.group) * D + 4 * tx;
+#pragma unroll
+        for (int n = 0; n < NC; ++n)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) dst[64 * n + k] = from_f<T>(o[i][4 * n + k] * inv);
+      } else {
+        const size_t at = (size_t)jb.slot * ws.rows_cap + r;
+#pragma unroll
+        for (int n = 0; n < NC; ++n)
+          *reinterpret_cast<float4*>(ws.o + at * D + 4 * tx + 64 * n) =
+              make_float4(o[i][4 * n], o[i][4 * n + 1], o[i][4 * n + 2], o[i][4 * n + 3]);
+        if (tx == 0) *reinterpret_cast<float2*>(ws.ml + 2 * at) = make_float2(m[i], l[i]);
+      }
+    }
+    __syncthreads();                            // job and queries are read
+  }
+}
+
+// ---------------------------------------------------------------- merge
+// Block (c, y) merges rows of the split item that starts in share c: the
+// states of its portions, in key order, so the result does not depend on
+// which CTA ran first.  Items of up to 8 portions: a warp a row; more: the
+// block's 8 warps take every 8th portion of a row each.  Reads a few hundred
+// KB; bound by latency.
+constexpr int kCombineThreads = 256;
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kCombineThreads)
+paged_combine_kernel(Params p, Workspace ws, T* __restrict__ O) {
+  pdl_wait();
+  pdl_trigger();
+  constexpr int V = D / 32;
+  __shared__ int slots[2 * Limits::kCtasSimt];
+  __shared__ int count;
+  __shared__ float red[8][D + 2];
+  const Desc d = ws.desc[blockIdx.x];
+  if (!d.valid) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // the portions' slots, in key order
+  if (warp == 0) {
+    const int64_t end_tiles = d.start + (int64_t)d.nt * d.unit;
+    int n = 1;
+    if (lane == 0) slots[0] = d.slot;
+    for (int base = blockIdx.x + 1; base < d.parts; base += 32) {
+      const int c = base + lane;
+      bool in = false, over = true;
+      if (c < d.parts) {
+        const int64_t a = share_start(d.total, d.parts, c), b = share_start(d.total, d.parts, c + 1);
+        over = a >= end_tiles;
+        const int ta = (int)min((int64_t)d.nt, (a - d.start) / d.unit);
+        const int tb = (int)min((int64_t)d.nt, (b - d.start) / d.unit);
+        in = !over && ta < tb;
+      }
+      const unsigned who = __ballot_sync(0xffffffffu, in);
+      if (in) slots[n + __popc(who & ((1u << lane) - 1u))] = 2 * c;
+      n += __popc(who);
+      if (__any_sync(0xffffffffu, over)) break;
+    }
+    if (lane == 0) count = n;
+  }
+  __syncthreads();
+  const int n = count;
+  const bool by_warp = n <= 8;
+  const int step = by_warp ? 8 * gridDim.y : gridDim.y;
+  for (int r = by_warp ? blockIdx.y * 8 + warp : blockIdx.y; r < d.rv; r += step) {
+    float mx = -INFINITY;
+    for (int k = lane; k < n; k += 32) mx = fmaxf(mx, ws.ml[2 * ((size_t)slots[k] * ws.rows_cap + r)]);
+    mx = warp_max(mx);
+    const float base = mx == -INFINITY ? 0.f : mx;
+    float acc[V], sum = 0.f;
+#pragma unroll
+    for (int e = 0; e < V; ++e) acc[e] = 0.f;
+#pragma unroll 4
+    for (int k = by_warp ? 0 : warp; k < n; k += by_warp ? 1 : 8) {
+      const size_t at = (size_t)slots[k] * ws.rows_cap + r;
+      const float2 ml = *reinterpret_cast<const float2*>(ws.ml + 2 * at);
+      const float f = fast_exp2(ml.x - base);
+      const float* src = ws.o + at * D + V * lane;
+      float x[V];
+#pragma unroll
+      for (int e = 0; e < V; e += 2) {
+        const float2 y = *reinterpret_cast<const float2*>(src + e);
+        x[e] = y.x;
+        x[e + 1] = y.y;
+      }
+      if (ml.x == -INFINITY) continue;          // no visible key in this portion
+      sum = fmaf(ml.y, f, sum);
+#pragma unroll
+      for (int e = 0; e < V; ++e) acc[e] = fmaf(x[e], f, acc[e]);
+    }
+    if (!by_warp) {
+      __syncthreads();
+#pragma unroll
+      for (int e = 0; e < V; ++e) red[warp][V * lane + e] = acc[e];
+      if (lane == 0) red[warp][D] = sum;
+      __syncthreads();
+      if (warp > 0) continue;
+      sum = 0.f;
+#pragma unroll
+      for (int e = 0; e < V; ++e) acc[e] = 0.f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        sum += red[k][D];
+#pragma unroll
+        for (int e = 0; e < V; ++e) acc[e] += red[k][V * lane + e];
+      }
+    }
+    const float inv = sum > 0.f ? 1.0f / sum : (sum == 0.f ? 0.f : sum);
+    const int rr = d.r0 + r;
+    T* dst = O + ((int64_t)(d.row0 + rr / p.group) * p.Hq + d.h * p.group + rr % p.group) * D + V * lane;
+#pragma unroll
+    for (int e = 0; e < V; ++e) dst[e] = from_f<T>(acc[e] * inv);
+  }
+}
+
+// ---------------------------------------------------------------- host side
+
+// rows an item may hold in the workspace: never more than the call has
+int rows_cap(const sa_paged_shape& s, int bm) {
+  const int64_t rows = (int64_t)s.T * (s.Hq / s.Hkv);
+  return (int)std::min<int64_t>(bm, (rows + 7) / 8 * 8);
+}
+
+constexpr size_t kDescBytes = (sizeof(Desc) * Limits::kCtasSimt + 255) / 256 * 256;
+
+size_t workspace_bytes(const sa_paged_shape& s) {
+  const size_t tc = (size_t)2 * Limits::kCtas * rows_cap(s, 256);
+  const size_t simt = (size_t)2 * Limits::kCtasSimt * rows_cap(s, SimtTiling::BM);
+  return kDescBytes + std::max(tc, simt) * (s.d + 2) * sizeof(float);
+}
+
+template <typename T, int D>
+sa_status launch_simt(const void* Q, int64_t q_stride, const void* Kc, const void* Vc, const sa_paged_shape& s,
+                      const Params& p, float scale, void* O, const Workspace& ws, cudaStream_t stream) {
+  constexpr size_t smem = simt_smem<D>();
+  static_assert(smem >= kMaxRequests * sizeof(int64_t), "the line lies in the operand buffers");
+  auto kern = paged_attn_simt_kernel<T, D>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    return launch_status("cudaFuncSetAttribute(paged_attn_simt_kernel)");
+  const cudaError_t le =
+      launch_pdl(kern, dim3(ws.ctas), dim3(kSimtThreads), smem, stream, static_cast<const T*>(Q), q_stride,
+                 static_cast<const T*>(Kc), static_cast<const T*>(Vc), p, scale * kLog2e, static_cast<T*>(O), ws);
+  if (le != cudaSuccess) return fail(SA_ERR_CUDA, std::string("paged_attn_simt_kernel: ") + cudaGetErrorString(le));
+  return launch_status("paged_attn_simt_kernel");
+}
+
+template <typename T, int D>
+sa_status launch_combine(const Params& p, const Workspace& ws, void* O, cudaStream_t stream) {
+  const int y = std::max(1, std::min(32, ws.rows_cap / 8));
+  const cudaError_t le = launch_pdl(paged_combine_kernel<T, D>, dim3(ws.ctas, y), dim3(kCombineThreads), 0, stream, p,
+                                    ws, static_cast<T*>(O));
+  if (le != cudaSuccess) return fail(SA_ERR_CUDA, std::string("paged_combine_kernel: ") + cudaGetErrorString(le));
+  return launch_status("paged_combine_kernel");
+}
+
+sa_status check_attn_shape(const sa_paged_shape& s, sa_dtype dtype, const char* fn) {
+  sa_status r = check_paged_heads(s, dtype, fn);
+  if (r != SA_OK) return r;
+  if (s.Hq <= 0 || s.Hq % s.Hkv)
+    return fail(SA_ERR_INVALID_ARG, std::string(fn) + ": Hq must be a positive multiple of Hkv");
+  if ((int64_t)s.T * s.Hq > (1 << 30))
+    return fail(SA_ERR_UNSUPPORTED, std::string(fn) + ": T * Hq exceeds 2^30 query rows");
+  return SA_OK;
+}
+
+}  // namespace
+}  // namespace sa
+
+extern "C" size_t sa_paged_attn_workspace_size(sa_paged_shape shape) {
+  using namespace sa;
+  if (check_attn_shape(shape, SA_BF16, "sa_paged_attn_workspace_size") != SA_OK) return 0;
+  return workspace_bytes(shape);
+}
+
+extern "C" sa_status sa_paged_attn_fwd(const void* Q, int64_t q_row_stride, const void* Kcache, const void* Vcache,
+                                       sa_dtype dtype, sa_paged_shape shape, const int32_t* q_start,
+                                       const int32_t* kv_len, const int32_t* table, int32_t window, float scale,
+                                       void* O, void* workspace, size_t workspace_bytes_given, void* stream) {
+  using namespace sa;
+  using namespace sa::paged;
+  sa_status r = check_attn_shape(shape, dtype, "sa_paged_attn_fwd");
+  if (r != SA_OK) return r;
+  if (window < 0) return fail(SA_ERR_INVALID_ARG, "sa_paged_attn_fwd: window must be 0 (none) or positive");
+  if (shape.T == 0 || shape.S == 0) return SA_OK;   // no row belongs to a request
+  if (!Q || !q_start || !kv_len || !O || (shape.P > 0 && shape.max_pages > 0 && (!Kcache || !Vcache || !table)))
+    return fail(SA_ERR_INVALID_ARG, "sa_paged_attn_fwd: Q, caches, q_start, kv_len, table and O are required");
+  const int64_t e = (int64_t)dtype_size(dtype);
+  if (shape.T > 1 && q_row_stride < (int64_t)shape.Hq * shape.d)
+    return fail(SA_ERR_INVALID_ARG, "sa_paged_attn_fwd: q_row_stride is smaller than Hq * d");
+  if (!aligned16(Q) || !aligned16(Kcache) || !aligned16(Vcache) || !aligned16(O) || (q_row_stride * e) % 16)
+    return fail(SA_ERR_ALIGNMENT, "sa_paged_attn_fwd: pointers and q_row_stride must be 16-byte aligned");
+  for (const void* x : {(const void*)q_start, (const void*)kv_len, (const void*)table})
+    if (reinterpret_cast<uintptr_t>(x) & 3u)
+      return fail(SA_ERR_ALIGNMENT, "sa_paged_attn_fwd: q_start, kv_len and table must be 4-byte aligned");
+  if (!workspace || workspace_bytes_given < workspace_bytes(shape))
+    return fail(SA_ERR_WORKSPACE, "sa_paged_attn_fwd: workspace missing or smaller than sa_paged_attn_workspace_size()");
+  if (reinterpret_cast<uintptr_t>(workspace) & 255u)
+    return fail(SA_ERR_ALIGNMENT, "sa_paged_attn_fwd: workspace must be 256-byte aligned");
+  // a pool or table without pages holds no key: every length reads as 0
+  const bool keys = shape.P > 0 && shape.max_pages > 0;
+  const int shift = 31 - __builtin_clz((unsigned)shape.page);
+  const int most = keys ? shape.max_pages << shift : 0;
+  Params p{q_start, kv_len, table, shape.S, shape.T, shape.Hq, shape.Hkv, shape.Hq / shape.Hkv, shift, shape.P,
+           keys ? shape.max_pages : 0, window >= most ? 0 : window};
+  Workspace ws;
+  ws.desc = static_cast<Desc*>(workspace);
+  const bool tc = false;
+  ws.rows_cap = rows_cap(shape, tc ? 256 : SimtTiling::BM);
+  ws.ctas = tc ? Limits::kCtas : Limits::kCtasSimt;
+  ws.o = reinterpret_cast<float*>(static_cast<char*>(workspace) + kDescBytes);
+  ws.ml = ws.o + (size_t)2 * ws.ctas * ws.rows_cap * shape.d;
+  cudaStream_t st = as_stream(stream);
+  if (dtype == SA_FP32) {
+    r = shape.d == 128 ? launch_simt<float, 128>(Q, q_row_stride, Kcache, Vcache, shape, p, scale, O, ws, st)
+                       : launch_simt<float, 64>(Q, q_row_stride, Kcache, Vcache, shape, p, scale, O, ws, st);
+    if (r != SA_OK) return r;
+    return shape.d == 128 ? launch_combine<float, 128>(p, ws, O, st) : launch_combine<float, 64>(p, ws, O, st);
+  }
+  using bf = __nv_bfloat16;
+  r = shape.d == 128 ? launch_simt<bf, 128>(Q, q_row_stride, Kcache, Vcache, shape, p, scale, O, ws, st)
+                     : launch_simt<bf, 64>(Q, q_row_stride, Kcache, Vcache, shape, p, scale, O, ws, st);
+  if (r != SA_OK) return r;
+  return shape.d == 128 ? launch_combine<bf, 128>(p, ws, O, st) : launch_combine<bf, 64>(p, ws, O, st);
+}

@@ -1,9 +1,10 @@
 """The hot path as a sequence of C-ABI calls with preallocated buffers.
 
 A prefill step is block_pool -> route -> sparse_attn_fwd; a decode step is
-decode_fwd over precomputed cache statistics.  The buffers are allocated once
-(torch device memory) and every call goes through ``binding``; nothing here
-computes.
+decode_fwd over precomputed cache statistics.  A serving step over a paged
+cache is paged_plan -> paged_append -> paged_attn_fwd.  The buffers are
+allocated once (torch device memory) and every call goes through ``binding``;
+nothing here computes.
 """
 
 from __future__ import annotations
@@ -151,3 +152,51 @@ class Fp8PrefillStep:
 
     def launches(self) -> int:
         return 2 + 5 + 1
+
+
+class PagedServing:
+    """A paged KV cache with its free pages, and the steps of a server on it.
+
+    ``requests`` rows of the table, each of up to ``max_pages`` pages, share
+    ``pages`` pages of ``page`` tokens; a step brings up to ``tokens`` rows.
+    A step is ``plan`` once and then, per layer, ``attend`` (append and
+    attention); the cache here is that of one layer, and further layers share
+    the plan through their own pools.  Lengths stay on the device, so a
+    captured step replays with other lengths.
+    """
+
+    def __init__(self, requests: int, max_pages: int, pages: int, page: int, tokens: int, Hq: int, Hkv: int, d: int,
+                 dtype=torch.bfloat16, device="cuda"):
+        dev = torch.device(device)
+        if dev.type == "cuda" and dev.index is None:
+            dev = torch.device("cuda", torch.cuda.current_device())
+        i = dict(device=dev, dtype=torch.int32)
+        self.page, self.tokens = page, tokens
+        self.Kcache = torch.empty(pages, Hkv, page, d, device=dev, dtype=dtype)
+        self.Vcache = torch.empty_like(self.Kcache)
+        self.held = torch.zeros(requests, **i)
+        self.table = torch.full((requests, max_pages), -1, **i)
+        self.free_pages = torch.arange(pages, **i)
+        self.free_state = torch.tensor([0, pages], **i)
+        self.q_start = torch.zeros(requests + 1, **i)
+        self.kv_len = torch.zeros(requests, **i)
+        self.slots = torch.full((tokens,), -1, device=dev, dtype=torch.int64)
+        ws = bd.paged_attn_workspace_size(requests, tokens, Hq, Hkv, d, page, pages, max_pages)
+        self.workspace = torch.empty(max(ws, 256), device=dev, dtype=torch.uint8)
+        self.out = torch.zeros(tokens, Hq, d, device=dev, dtype=dtype)
+
+    def plan(self, ctx_len, new_len, stream=None):
+        """Pages and slots for new_len[s] more tokens of each request (see binding.paged_plan)."""
+        return bd.paged_plan(ctx_len, new_len, self.held, self.table, self.free_pages, self.free_state, self.tokens,
+                             self.page, q_start=self.q_start, kv_len=self.kv_len, slots=self.slots, stream=stream)
+
+    def attend(self, Q, K, V, scale: float, *, window: int = 0, caches=None, out=None, stream=None):
+        """Appends the planned step's K, V and attends from Q; ``caches``: another layer's (Kcache, Vcache)."""
+        Kc, Vc = caches if caches is not None else (self.Kcache, self.Vcache)
+        bd.paged_append(K, V, self.slots, Kc, Vc, stream=stream)
+        return bd.paged_attn_fwd(Q, Kc, Vc, self.table, self.q_start, self.kv_len, scale, window=window,
+                                 out=self.out if out is None else out, workspace=self.workspace, stream=stream)
+
+    # kernels a plan and an attend launch (plan; append, attention, merge)
+    def launches(self) -> int:
+        return 4

@@ -416,6 +416,103 @@ size_t sa_sfa_workspace_size(sa_shape shape);
 sa_status sa_sfa_attn_fwd(const void* Qs, const void* Ks, const void* V, sa_dtype dtype, sa_shape shape,
                           float scale, void* O, void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---- Paged KV cache -------------------------------------------------------
+ *
+ * Serving: requests of different lengths, caches that grow, prompts taken in
+ * chunks.  The caches are pools of P pages of `page` tokens, [P,Hkv,page,d]
+ * for K and for V; request s owns the pages table[s][0 .. ceil(len / page)).
+ * The rows of a step's new tokens are packed, request behind request: request
+ * s has rows q_start[s] .. q_start[s+1] of the T rows that the arrays hold;
+ * rows from q_start[S] on are padding.  A step is sa_paged_plan (pages and
+ * places for the new tokens), sa_paged_append (their K and V) and
+ * sa_paged_attn_fwd (their attention); lengths stay on the device, so the
+ * three calls can be captured into a graph and replayed with other lengths.
+ *
+ * S <= 4096 requests; page in {16, 32, 64, 128}; d in {64, 128}; Hq any
+ * multiple of Hkv; max_pages * page <= 2^30; S * max_pages, P * Hkv and
+ * T * Hkv below 2^31, T * Hq <= 2^30 (else SA_ERR_UNSUPPORTED).  Lengths,
+ * tables, slots and the free ring are read on the device and bounded there:
+ * whatever they hold, nothing outside the given arrays is read or written. */
+typedef struct {
+  int32_t S;          /* requests                                     */
+  int32_t T;          /* rows of the packed arrays (padding included) */
+  int32_t Hq, Hkv, d;
+  int32_t page;       /* tokens per page                              */
+  int32_t P;          /* pages of the pools                           */
+  int32_t max_pages;  /* columns of the table                         */
+} sa_paged_shape;
+
+/* Plan of a step: request s has ctx_len[s] tokens in its pages and brings
+ * new_len[s] rows.  Its pages become ceil((ctx + new) / page): missing ones
+ * are taken from the free ring in request order, surplus ones are handed back
+ * (new = 0 and a smaller ctx shortens a request, ctx = new = 0 ends it).
+ * Updated in place:
+ *   held [S]            pages that each request owns (0 for an empty row)
+ *   table [S,max_pages] taken pages are entered, returned ones become -1
+ *   free_pages [P]      ring of the free pages
+ *   free_state [2]      {position of the first free page, number of free pages}
+ * Pages returned by a call can be taken from the next call on.  Written:
+ *   q_start [S+1]  exclusive prefix sum of new_len, at most T
+ *   kv_len [S]     ctx_len + new_len, or 0 for a refused request
+ *   slots [T]      int64 place of each row in the pools, page id * page +
+ *                  offset; -1 for padding and for rows of refused requests
+ * A request is refused when a length is negative, when it needs more than
+ * max_pages pages, when its rows end behind T, or when the pages asked for up
+ * to and including it (refused ones too) are more than the free ones; its
+ * pages, its table row and held[s] stay as they are, and its rows keep their
+ * places in q_start.  Hq, Hkv and d of the shape are not used.  The arrays
+ * must not overlap.
+ * Errors: SA_ERR_INVALID_ARG (S, P or max_pages not positive, a null array),
+ *         SA_ERR_UNSUPPORTED, SA_ERR_ALIGNMENT (element alignment). */
+sa_status sa_paged_plan(const int32_t* ctx_len, const int32_t* new_len, sa_paged_shape shape, int32_t* held,
+                        int32_t* table, int32_t* free_pages, int32_t* free_state, int32_t* q_start,
+                        int32_t* kv_len, int64_t* slots, void* stream);
+
+/* Writes the rows K, V [T,Hkv,d] (row t at K + t * k_row_stride elements, the
+ * heads of a row contiguous, so that views of one fused projection serve) to
+ * their slots: Kcache[slot / page][h][slot % page][:] = K[t][h][:], V alike.
+ * Rows whose slot lies outside [0, P * page) are skipped.  The slots of a
+ * call should differ; of rows with the same slot any one's values may remain,
+ * element by element.  Hq of the shape is not used.
+ * Errors: SA_ERR_INVALID_ARG (null array, a stride below Hkv * d),
+ *         SA_ERR_UNSUPPORTED, SA_ERR_ALIGNMENT (16 bytes for tensors and row
+ *         strides, 8 for slots). */
+sa_status sa_paged_append(const void* K, const void* V, int64_t k_row_stride, int64_t v_row_stride,
+                          sa_dtype dtype, sa_paged_shape shape, const int64_t* slots, void* Kcache,
+                          void* Vcache, void* stream);
+
+/* Bytes of workspace sa_paged_attn_fwd needs (0 on bad arguments); at most
+ * 39 MiB. */
+size_t sa_paged_attn_workspace_size(sa_paged_shape shape);
+
+/* Attention of the step's rows over their request's cache.  Row i of request
+ * s (n = q_start[s+1] - q_start[s] rows) has position p = kv_len[s] - n + i
+ * and sees the keys max(0, p - window + 1) .. p (window 0: from 0 on); query
+ * head h reads KV head h / (Hq / Hkv):
+ *   o = sum e^{scale q.k} v / sum e^{scale q.k}   over the keys it sees,
+ * 0 for a row that sees none (kv_len[s] < n - i; a refused request).  One
+ * row per request is decoding, several are a chunk of a prompt, and a call
+ * may mix them.  Q: [T,Hq,d] with row stride q_row_stride (elements), the
+ * heads of a row contiguous; O: [T,Hq,d] contiguous; rows from q_start[S] on
+ * are left as they were.  Q, caches and O of `dtype`: bf16 runs on the tensor
+ * cores (p rounded to bf16 for the second product), fp32 on CUDA cores; maxima,
+ * sums and outputs are held in float32.  A key that no row of a request sees
+ * (behind kv_len, left of the window) is never used, whatever its memory
+ * holds, and a key that a row does not see does not reach that row, also
+ * where its K or V is not finite.  A table entry outside [0, P) under a
+ * visible key makes that request's output unspecified.  q_start is read as
+ * q_start[s] clamped to [0, T], kv_len to [0, max_pages * page]; requests
+ * whose row ranges overlap leave either one's output.  workspace:
+ * at least sa_paged_attn_workspace_size() bytes, 256-byte aligned, contents
+ * on entry do not matter; calls that may run at the same time need one each.
+ * The result does not depend on scheduling (no atomics).
+ * Errors: SA_ERR_INVALID_ARG, SA_ERR_UNSUPPORTED, SA_ERR_ALIGNMENT,
+ *         SA_ERR_WORKSPACE. */
+sa_status sa_paged_attn_fwd(const void* Q, int64_t q_row_stride, const void* Kcache, const void* Vcache,
+                            sa_dtype dtype, sa_paged_shape shape, const int32_t* q_start,
+                            const int32_t* kv_len, const int32_t* table, int32_t window, float scale,
+                            void* O, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Reads and clears the library's device-side error word (synchronous: waits
  * for work already queued on the legacy default stream).  Non-zero means a
  * kernel gave up on an internal wait (bit 0: a bounded barrier wait timed

@@ -35,3 +35,4 @@ from .sparse_attention import (  # noqa: F401
 )
 from .feature_sparse import sfa_codes, sfa_densify, sfa_attention  # noqa: F401
 from .backward import sparse_attention_backward, sparse_attention_lse  # noqa: F401
+from .paged import paged_plan, paged_append, paged_attention  # noqa: F401

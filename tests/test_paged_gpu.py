@@ -1,0 +1,435 @@
+"""The paged KV cache on the GPU against the float64 oracle: plan, append,
+attention, and serving steps that run them together.
+
+Tolerances of the attention, elementwise against A = Σ p |v| / Σ p:
+bf16: the weights p are rounded to bf16 (2^-8) from exponentials good to
+7.5e-5, the row sums use the unrounded weights (7.5e-5 again), the fp32 sums
+add at most keys · 2^-24 each, and the output is rounded once (2^-8 |o|).
+fp32: a score is a dot product of d terms in fp32 and its exponential is good
+to 2^-21, so a weight is off by (d + 4) 2^-24 Σ|q_c k_c| scale + 2^-21, the
+numerator and the row sum each, plus keys · 2^-24 for either sum.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from block_sparse_approximate_b200 import binding as bd
+from block_sparse_approximate_b200.pipeline import PagedServing
+from tests._parity import assert_no_device_error, np64
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def _i32(a):
+    return torch.from_numpy(np.asarray(a)).to(device=DEV, dtype=torch.int32)
+
+
+class Case:
+    """Pools with the requests' pages in random places; everything that no row may use is poisoned with NaN."""
+
+    def __init__(self, ctx, new, Hq, Hkv, d, page, dtype, seed, *, pad=0, spare=3, refuse=(), window=0, wide=0, poison=True):
+        g = torch.Generator(device=DEV)
+        g.manual_seed(seed)
+        ctx, new = np.asarray(ctx), np.asarray(new)
+        S, T = len(ctx), int(new.sum()) + pad
+        kv = ctx + new
+        kv[list(refuse)] = 0
+        n_pages = -(-kv // page)
+        P = int(n_pages.sum()) + spare
+        perm = torch.randperm(P, generator=g, device=DEV).cpu().numpy()
+        self.table = np.full((S, int(n_pages.max()) + 1), -1)
+        at = 0
+        for s in range(S):
+            self.table[s, :n_pages[s]] = perm[at:at + n_pages[s]]
+            at += n_pages[s]
+        rnd = lambda *s: torch.randn(*s, generator=g, device=DEV).to(dtype)  # noqa: E731
+        # Q as a view of wider rows
+        self.Q = rnd(T, Hq + wide, d)[:, wide // 2:wide // 2 + Hq]
+        self.Kc, self.Vc = rnd(P, Hkv, page, d), rnd(P, Hkv, page, d)
+        if poison:
+            used = torch.zeros(P, page, dtype=torch.bool)
+            for s in range(S):
+                n = int(new[s])
+                lo = max(0, int(kv[s]) - n - window + 1) if window else 0
+                for k in range(lo, int(kv[s])):
+                    used[self.table[s, k // page], k % page] = True
+            hole = ~used.to(DEV)[:, None, :, None]
+            for c in (self.Kc, self.Vc):
+                c.masked_fill_(hole, float("nan"))
+        self.q_start = np.concatenate([[0], np.cumsum(new)])
+        self.kv, self.window, self.scale, self.dtype, self.d = kv, window, 1 / math.sqrt(d), dtype, d
+        self.T, self.Hq = T, Hq
+
+    def run(self, **kw):
+        self.lists = [_i32(a) for a in (self.table, self.q_start, self.kv)]   # kept while another stream reads them
+        if "stream" in kw:
+            torch.cuda.synchronize()
+        return bd.paged_attn_fwd(self.Q, self.Kc, self.Vc, *self.lists, self.scale, window=self.window, **kw)
+
+    def oracle(self):
+        return oracle.paged_attention(np64(self.Q), np64(self.Kc), np64(self.Vc), self.table, self.q_start, self.kv,
+                                      self.scale, self.window)
+
+    def check(self, out, fill=7.0):
+        O, A, seen = self.oracle()
+        assert_attention(out, O, A, seen, self, fill)
+
+
+def largest_score(c):
+    """A bound on Σ|q_c k_c| scale: |q| |k| scale (Cauchy-Schwarz) of the largest rows."""
+    q, k = np64(c.Q), np.nan_to_num(np64(c.Kc))
+    return np.sqrt((q ** 2).sum(-1)).max() * np.sqrt((k ** 2).sum(-1)).max() * c.scale
+
+
+def assert_attention(out, O, A, seen, c, fill):
+    got = np64(out)
+    rows = seen >= 0
+    assert (got[~rows] == fill).all(), "rows of no request were written"
+    assert (got[seen == 0] == 0).all(), "a row without keys is zero"
+    rows = seen > 0
+    if not rows.any():
+        return
+    keys = seen[rows].astype(np.float64)[:, None, None]
+    if c.dtype == BF:
+        w = 2.0 ** -8 + 2 * 7.5e-5 + 2 * keys * 2.0 ** -24
+        bound = w * A[rows] + 2.0 ** -8 * np.abs(O[rows]) * (1 + w) + 1e-30
+    else:
+        w = (c.d + 4) * 2.0 ** -24 * largest_score(c) + 2.0 ** -21 + keys * 2.0 ** -24
+        bound = 2 * w * A[rows] + 2.0 ** -23 * np.abs(O[rows]) + 1e-30
+    assert np.isfinite(got[rows]).all(), "non-finite output"
+    worst = float((np.abs(got[rows] - O[rows]) / bound).max())
+    assert worst <= 1.0, f"error reaches {worst:.2f} of the bound"
+
+
+SHAPES = [(BF, 128, 8, 2), (BF, 64, 4, 4), (F32, 128, 6, 2), (F32, 64, 4, 4)]
+LENS = {
+    "one_token": ([0], [1]),
+    "decode": ([0, 1, 15, 16, 63, 64, 127, 128, 200, 1000], [1] * 10),
+    "idle_requests": ([0, 40, 0, 77, 5], [0, 0, 3, 1, 0]),
+    "prompts": ([0, 0, 0], [1, 129, 300]),
+    "chunks": ([5, 127, 128, 1000], [60, 129, 128, 37]),
+    "mixed": ([700, 31, 0, 513, 64, 9], [1, 200, 17, 1, 1, 64]),
+}
+
+
+@pytest.mark.parametrize("lens", sorted(LENS))
+@pytest.mark.parametrize("dtype,d,Hq,Hkv", SHAPES)
+@pytest.mark.parametrize("page", [16, 64])
+def test_attention(lib, lens, dtype, d, Hq, Hkv, page):
+    ctx, new = LENS[lens]
+    c = Case(ctx, new, Hq, Hkv, d, page, dtype, seed=1, pad=3, wide=2 * Hkv)
+    out = torch.full((c.T, Hq, d), 7.0, device=DEV, dtype=dtype)
+    assert c.run(out=out) is out
+    torch.cuda.synchronize()
+    assert_no_device_error()
+    c.check(out)
+
+
+@pytest.mark.parametrize("page", [32, 128])
+@pytest.mark.parametrize("group", [1, 3, 5, 7, 16, 33])
+def test_attention_group_sizes(lib, page, group):
+    # query heads per KV head that divide no tile, and more of them than a quarter tile
+    c = Case([130, 5, 300, 0], [1, 70, 9, 2], 2 * group, 2, 128, page, BF, seed=2, pad=1)
+    out = torch.full((c.T, c.Hq, 128), 7.0, device=DEV, dtype=BF)
+    c.run(out=out)
+    c.check(out)
+
+
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (BF, 64), (F32, 64)])
+@pytest.mark.parametrize("window", [1, 2, 17, 128, 129, 1000])
+def test_attention_window(lib, dtype, d, window):
+    c = Case([0, 700, 1200, 40, 999], [150, 300, 1, 20, 2], 4, 2, d, 16, dtype, seed=3, pad=2, window=window)
+    out = torch.full((c.T, 4, d), 7.0, device=DEV, dtype=dtype)
+    c.run(out=out)
+    torch.cuda.synchronize()
+    assert_no_device_error()
+    c.check(out)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_rows_that_see_no_key(lib, dtype):
+    # refused requests (kv_len 0) and a length below the number of rows: the first rows see nothing
+    c = Case([10, 300, 64], [5, 20, 1], 4, 2, 128, 32, dtype, seed=4, pad=1, refuse=(0,))
+    c.kv[1] = 12                                  # 20 rows, 12 keys: 8 rows at negative positions
+    c.Kc.nan_to_num_(0.5)
+    c.Vc.nan_to_num_(0.5)
+    out = torch.full((c.T, 4, 128), 7.0, device=DEV, dtype=dtype)
+    c.run(out=out)
+    c.check(out)
+    # no request has a row
+    c.q_start[:] = 0
+    out.fill_(7.0)
+    c.run(out=out)
+    assert (out == 7.0).all()
+
+
+@pytest.mark.parametrize("dtype,d,Hq", [(BF, 128, 8), (BF, 64, 2), (F32, 64, 4)])
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+def test_values_of_unseen_new_tokens(lib, dtype, d, Hq, bad):
+    # a later token of the same chunk holds values that are not finite: earlier rows do not see it
+    c = Case([100, 3, 260], [140, 40, 1], Hq, 2, d, 16, dtype, seed=5)
+    s, at = 0, 200                                # request 0, position 200 = row 100
+    pid, off = c.table[s, at // 16], at % 16
+    before = c.oracle()
+    c.Vc[pid, 1, off, 5] = bad
+    c.Kc[pid, 0, off, :] = bad
+    out = c.run()
+    torch.cuda.synchronize()
+    assert_no_device_error()
+    got = np64(out)
+    clean = np.ones((c.T, Hq, d), bool)
+    clean[100:140, :Hq // 2] = False              # rows that see the bad key
+    clean[100:140, Hq // 2:, 5] = False           # and the bad value
+    O, A, seen = before
+    err = np.abs(got - O)
+    bound = (2.0 ** -8 + 2e-4) * A + 2.0 ** -7 * np.abs(O) + 1e-6
+    assert np.isfinite(got[clean]).all()
+    assert (err[clean] <= bound[clean]).all()
+    hit = got[100:140, Hq // 2:, 5]
+    assert not np.isfinite(hit).any() and (np.isnan(hit).all() if math.isnan(bad) else (hit == bad).all())
+
+
+@pytest.mark.parametrize("dtype,Hq,Hkv", [(BF, 16, 2), (BF, 3, 1), (F32, 4, 2)])
+def test_long_contexts_split_over_many_ctas(lib, dtype, Hq, Hkv):
+    # few rows and many keys: every item is split, and merged in key order
+    c = Case([9000, 3, 20011], [1, 1, 4], Hq, Hkv, 128, 64, dtype, seed=6, poison=False)
+    a, b = c.run(), c.run()
+    torch.cuda.synchronize()
+    assert_no_device_error()
+    assert torch.equal(a, b)
+    c.check(a)
+
+
+def test_large_scores_and_shifts(lib):
+    # scores of some hundreds in either direction, the largest one late: running maxima move by far
+    c = Case([900, 300], [3, 150], 4, 2, 128, 32, BF, seed=7, poison=False)
+    c.Q = (c.Q.float() * 8).to(BF)
+    c.Kc = (c.Kc.float() * 8).to(BF)
+    out = c.run()
+    O, A, seen = c.oracle()
+    # here the fp32 rounding of the scores counts beside that of the weights
+    err = np.abs(np64(out) - O)
+    bound = (2.0 ** -8 + 2e-4 + 2 * 132 * 2.0 ** -24 * largest_score(c)) * A + 2.0 ** -7 * np.abs(O) + 1e-6
+    assert (err <= bound).all()
+
+
+def test_pools_beyond_32_bit_offsets(lib):
+    # the pool holds more than 2^31 elements and the requests' pages are its last ones
+    Hkv, page, d = 8, 128, 128
+    P = (1 << 31) // (Hkv * page * d) + 40
+    g = torch.Generator(device=DEV)
+    g.manual_seed(8)
+    Kc = torch.zeros(P, Hkv, page, d, device=DEV, dtype=BF)
+    Vc = torch.zeros_like(Kc)
+    small = Case([500, 130], [9, 1], 16, Hkv, d, page, BF, seed=8, spare=0, poison=False)
+    n = small.Kc.shape[0]
+    T = small.T
+    K, V = (torch.randn(T, Hkv, d, generator=g, device=DEV).to(BF) for _ in range(2))
+    Kc[-n:], Vc[-n:] = small.Kc, small.Vc
+    slots = np.concatenate([[small.table[0, p // page] * page + p % page for p in range(500, 509)],
+                            [small.table[1, 130 // page] * page + 130 % page]])
+    far = torch.from_numpy(slots + (P - n) * page).to(DEV)
+    bd.paged_append(K, V, far, Kc, Vc)
+    bd.paged_append(K, V, torch.from_numpy(slots).to(DEV), small.Kc, small.Vc)
+    assert torch.equal(Kc[-n:], small.Kc) and torch.equal(Vc[-n:], small.Vc)
+    assert int(torch.count_nonzero(Kc[:-n])) == 0
+    small.table = np.where(small.table >= 0, small.table + P - n, -1)
+    got = bd.paged_attn_fwd(small.Q, Kc, Vc, _i32(small.table), _i32(small.q_start), _i32(small.kv), small.scale)
+    small.table = np.where(small.table >= 0, small.table - (P - n), -1)
+    small.check(got)
+
+
+def test_table_entries_outside_the_pool_read_nothing(lib):
+    # documented as unspecified output of that request; the other one is unharmed
+    for dtype in (BF, F32):
+        c = Case([100, 90], [40, 1], 4, 2, 64, 32, dtype, seed=9, poison=False)
+        c.table[0, 1], c.table[0, 2] = 1 << 30, -5
+        out = c.run()
+        torch.cuda.synchronize()
+        c.table[0, 1], c.table[0, 2] = 0, 0
+        O, A, _ = c.oracle()
+        err = np.abs(np64(out) - O)[40:]
+        assert (err <= (2.0 ** -7 + 1e-3) * A[40:]).all()
+        assert_no_device_error()
+
+
+# --------------------------------------------------------------------------
+# append
+# --------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype,d,Hkv,page,T", [(BF, 128, 8, 16, 1), (BF, 64, 3, 32, 77), (F32, 128, 1, 64, 200),
+                                                (F32, 64, 5, 128, 1000), (BF, 128, 8, 64, 3000)])
+def test_append(lib, dtype, d, Hkv, page, T):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(T)
+    P = -(-T // page) + 5
+    rnd = lambda *s: torch.randn(*s, generator=g, device=DEV).to(dtype)  # noqa: E731
+    fused = rnd(T, 3 * Hkv + 1, d)
+    K, V = fused[:, Hkv:2 * Hkv], fused[:, 2 * Hkv:3 * Hkv]
+    Kc, Vc = rnd(P, Hkv, page, d), rnd(P, Hkv, page, d)
+    slots = torch.randperm(P * page, generator=g, device=DEV)[:T].clone()
+    slots[::7] = -1
+    if T > 5:
+        slots[3], slots[5] = P * page, 1 << 40      # behind the pool: skipped
+    rK, rV = oracle.paged_append(np64(K), np64(V), slots.cpu().numpy(), np64(Kc), np64(Vc))
+    bd.paged_append(K, V, slots, Kc, Vc)
+    np.testing.assert_array_equal(np64(Kc), rK)
+    np.testing.assert_array_equal(np64(Vc), rV)
+    # K and V with row strides of their own
+    K2 = K.contiguous()
+    bd.paged_append(K2, V, slots, Kc, Vc)
+    np.testing.assert_array_equal(np64(Kc), rK)
+
+
+# --------------------------------------------------------------------------
+# plan
+# --------------------------------------------------------------------------
+
+@pytest.mark.parametrize("S,width,P,page,tokens", [(1, 5, 4, 16, 1), (9, 7, 30, 16, 120), (33, 40, 500, 32, 1500),
+                                                   (300, 9, 1000, 64, 257), (1025, 4, 3000, 128, 9000),
+                                                   (4096, 3, 6000, 16, 20000)])
+def test_plan(lib, S, width, P, page, tokens):
+    r = np.random.RandomState(S)
+    held, table = np.zeros(S, int), np.full((S, width), -1)
+    ring, state = r.permutation(P), np.array([P // 3, P])
+    d = [_i32(a) for a in (held, table, ring, state)]
+    length = np.zeros(S, int)
+    some = 0
+    for step in range(8):
+        ctx = np.where(r.rand(S) < 0.2, length // 2, length)
+        ctx = np.where(r.rand(S) < 0.1, 0, ctx)
+        new = r.randint(0, max(2, 2 * tokens // S), S) * (r.rand(S) < 0.6)
+        if step == 3:
+            ctx[S // 2], new[0] = -1, -4                        # lengths that are refused
+        if step == 5 and S > 8:
+            new[S - 1] = 2 ** 31 - 1                            # a sum that leaves 32 bits
+        *ref, held, table, ring, state = oracle.paged_plan(ctx, new, held, table, ring, state, tokens, page)
+        got = bd.paged_plan(_i32(ctx), _i32(new), *d, tokens, page)
+        for name, x, y in zip(("q_start", "kv_len", "slots", "held", "table", "ring", "state"), (*got, *d),
+                              (*ref, held, table, ring, state)):
+            np.testing.assert_array_equal(x.cpu().numpy(), y, err_msg=f"step {step}: {name}")
+        kv = ref[1]
+        fine = kv == ctx + new
+        length = np.where(fine, kv, length)
+        some += int((~fine).sum())
+    assert some > 0 or S == 1
+
+
+# --------------------------------------------------------------------------
+# serving steps
+# --------------------------------------------------------------------------
+
+def _serve(lib, dtype, stream=None, graph=False):
+    """Three requests through prompts in chunks, decoding, an end and a newcomer; every row against whole-request attention."""
+    r = np.random.RandomState(11)
+    Hq, Hkv, d, page = 6, 2, 64, 16
+    eng = PagedServing(requests=3, max_pages=20, pages=31, page=page, tokens=96, Hq=Hq, Hkv=Hkv, d=d, dtype=dtype)
+    scale = 1 / math.sqrt(d)
+    hist = [([], []) for _ in range(3)]
+    length = np.zeros(3, int)
+    ctx_d, new_d = _i32(np.zeros(3)), _i32(np.zeros(3))
+    fused = torch.zeros(96, Hq + 2 * Hkv, d, device=DEV, dtype=dtype)
+    Q, K, V = fused[:, :Hq], fused[:, Hq:Hq + Hkv], fused[:, Hq + Hkv:]
+    eng.Kcache.fill_(float("nan"))
+    eng.Vcache.fill_(float("nan"))
+
+    def step():
+        eng.plan(ctx_d, new_d, stream=stream)
+        eng.attend(Q, K, V, scale, stream=stream)
+    g = None
+    steps = [([0, 0, 0], [40, 1, 0]), (None, [50, 1, 33]), (None, [1, 1, 1]), (None, [1, 0, 70]),
+             ([91, -2, -2], [3, 1, 1]), ([0, -2, -2], [0, 5, 1]), (None, [64, 1, 1]), (None, [300, 2, 1])]
+    for n, (at, new) in enumerate(steps):
+        if at is not None:                          # a request's tokens are taken back, or it ends (-2: as it is)
+            for s, a in enumerate(at):
+                if a != -2:
+                    length[s] = a
+                    hist[s] = (hist[s][0][:a], hist[s][1][:a])
+        new = np.asarray(new)
+        rows = np.concatenate([[0], np.cumsum(new)])
+        ctx_d.copy_(_i32(length))
+        new_d.copy_(_i32(new))
+        fused.copy_(torch.from_numpy(r.randn(*fused.shape)).to(DEV))
+        eng.out.fill_(7.0)
+        torch.cuda.synchronize()
+        if not graph:
+            step()
+        elif g is None:
+            saved = [x.clone() for x in (eng.held, eng.table, eng.free_pages, eng.free_state, eng.Kcache, eng.Vcache)]
+            side = torch.cuda.Stream()
+            with torch.cuda.stream(side):
+                step()                              # warm-up on the capturing stream, then the state as it was
+            torch.cuda.synchronize()
+            for x, y in zip((eng.held, eng.table, eng.free_pages, eng.free_state, eng.Kcache, eng.Vcache), saved):
+                x.copy_(y)
+            eng.out.fill_(7.0)
+            torch.cuda.synchronize()
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g):
+                step()
+            g.replay()
+        else:
+            g.replay()
+        torch.cuda.synchronize()
+        assert_no_device_error()
+        kv = eng.kv_len.cpu().numpy()
+        out = np64(eng.out)
+        for s in range(3):
+            mine = slice(min(96, rows[s]), min(96, rows[s + 1]))
+            if kv[s] != length[s] + new[s]:         # refused: too many rows for the step
+                assert new[s] == 300 and kv[s] == 0 and (out[mine] == 0).all()
+                break
+            for a, b in zip(hist[s], (K, V)):
+                a.extend(np64(b[mine]))
+            length[s] += new[s]
+            if not new[s]:
+                continue
+            k, v = (np.array(x).transpose(1, 0, 2)[None] for x in hist[s])
+            O, A, seen = oracle.paged_attention(np64(Q[mine]), k, v, [[0]], [0, new[s]],
+                                                [length[s]], scale)
+            bound = (2.0 ** -8 + 2e-4) * A + 2.0 ** -7 * np.abs(O) + 1e-6
+            assert (np.abs(out[mine] - O) <= bound).all(), (n, s)
+        else:
+            assert (out[rows[-1]:] == 7.0).all()
+    return eng
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_serving_steps(lib, dtype):
+    _serve(lib, dtype)
+
+
+def test_serving_steps_captured(lib):
+    _serve(lib, BF, graph=True)
+
+
+def test_serving_steps_on_another_stream(lib):
+    _serve(lib, BF, stream=torch.cuda.Stream())
+
+
+def test_two_calls_at_once(lib):
+    # two streams, each with its own workspace
+    cs = [Case([3000, 10], [200, 1], 8, 2, 128, 64, BF, seed=s, poison=False) for s in (21, 22)]
+    alone = [c.run() for c in cs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cs]
+    got = [[c.run(stream=s) for _ in range(4)] for c, s in zip(cs, streams)]
+    torch.cuda.synchronize()
+    for a, many in zip(alone, got):
+        for b in many:
+            assert torch.equal(a, b)
+
+
+def test_call_from_another_current_stream_keeps_default(lib):
+    c = Case([100], [30], 4, 2, 128, 32, BF, seed=30, poison=False)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        a = c.run()
+    torch.cuda.synchronize()
+    assert torch.equal(a, c.run())
