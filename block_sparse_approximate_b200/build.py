@@ -38,14 +38,15 @@ def _headers():
     return sorted(glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h")))
 
 
-# attn_tc_kernel and attn_tc_linmix_kernel reallocate registers with
-# setmaxnreg: their launch register count times 384 threads must cover the
-# split (256 x 216 + 128 x 40, and 128 x 216 + 128 x 96 + 128 x 56; see
-# attn_tc.cu), or setmaxnreg.inc would wait for registers that never come.
-TC_MIN_LAUNCH_REGS = 158
+# attn_tc_kernel, attn_tc_linmix_kernel and paged_attn_tc_kernel reallocate
+# registers with setmaxnreg: their launch register count times 384 threads
+# must cover the split (256 x 216 + 128 x 40, and 128 x 216 + 128 x 96 +
+# 128 x 56, see attn_tc.cu; 256 x 208 + 128 x 88, see paged_attn_tc.cu), or
+# setmaxnreg.inc would wait for registers that never come.
+TC_MIN_LAUNCH_REGS = {"attn_tc.cu": 158, "paged_attn_tc.cu": 168}
 
 
-def _check_tc_registers(ptxas_log: str):
+def _check_tc_registers(ptxas_log: str, least: int):
     import re
     lines = ptxas_log.splitlines()
     for k, line in enumerate(lines):
@@ -54,9 +55,9 @@ def _check_tc_registers(ptxas_log: str):
                 m = re.search(r"Used (\d+) registers", nxt)
                 if m:
                     regs = int(m.group(1))
-                    if regs < TC_MIN_LAUNCH_REGS:
+                    if regs < least:
                         raise RuntimeError(f"attn_tc_kernel launches with {regs} registers per thread; "
-                                           f"the setmaxnreg split needs >= {TC_MIN_LAUNCH_REGS}")
+                                           f"the setmaxnreg split needs >= {least}")
                     break
 
 
@@ -76,7 +77,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         objs.append(obj)
         if force or _stale(obj, [src] + headers):
             extra = list(extra_flags)
-            if os.path.basename(src) == "attn_tc.cu" and "-v" not in extra:
+            if os.path.basename(src) in TC_MIN_LAUNCH_REGS and "-v" not in extra:
                 extra += ["-Xptxas", "-v"]
             cmd = [NVCC, *ARCH, *FLAGS, *extra, "-c", src, "-o", obj]
             jobs.append(cmd)
@@ -93,8 +94,9 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
                 print(r.stdout + r.stderr, flush=True)
             if r.returncode != 0:
                 raise RuntimeError("nvcc failed:\n" + " ".join(cmd) + "\n" + r.stdout + r.stderr)
-            if cmd[-3].endswith("attn_tc.cu"):
-                _check_tc_registers(r.stdout + r.stderr)
+            least = TC_MIN_LAUNCH_REGS.get(os.path.basename(cmd[-3]))
+            if least is not None:
+                _check_tc_registers(r.stdout + r.stderr, least)
     if force or jobs or _stale(LIB, objs):
         cmd = [NVCC, *ARCH, "-shared", "-o", LIB, *objs]
         r = subprocess.run(cmd, capture_output=True, text=True)

@@ -1285,6 +1285,19 @@ htot_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
 
 }  // namespace
 
+bool make_tmap_bf16_3d(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows, uint64_t outer,
+                       uint32_t box_cols, uint32_t box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {cols, rows, outer};
+  cuuint64_t strides[2] = {cols * 2, cols * rows * 2};
+  cuuint32_t box[3] = {box_cols, box_rows, 1};
+  cuuint32_t es[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool make_tmap_128x128(void* map, const void* base, int elem, uint64_t cols, uint64_t rows, uint64_t outer) {
   return make_tmap_3d(static_cast<CUtensorMap*>(map), base, elem, cols, rows, outer);
 }
@@ -1419,6 +1432,7 @@ extern "C" sa_status sa_device_error(uint32_t* code) {
   if (cudaMemcpyFromSymbol(&v, tc::g_device_error, sizeof(v)) != cudaSuccess ||
       cudaMemcpyToSymbol(tc::g_device_error, &zero, sizeof(zero)) != cudaSuccess)
     return launch_status("sa_device_error");
-  *code = v | decode_error_take() | covnorm_error_take() | bwd_error_take() | decode_tc_error_take();
+  *code = v | decode_error_take() | covnorm_error_take() | bwd_error_take() | decode_tc_error_take() |
+          paged_tc_error_take();
   return SA_OK;
 }

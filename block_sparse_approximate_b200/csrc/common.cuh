@@ -72,6 +72,8 @@ sa_status decode_stats_tc(const __nv_bfloat16* q, const void* kmean, const void*
                           float* scores, float* parta, int topk, int32_t* idx, bool* topk_done,
                           cudaStream_t stream);
 uint32_t decode_tc_error_take();
+// The same of the paged attention's tensor-core kernel (paged_attn_tc.cu).
+uint32_t paged_tc_error_take();
 
 // ---------------------------------------------------------------- device side
 

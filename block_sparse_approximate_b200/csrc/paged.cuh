@@ -232,6 +232,5 @@ struct Limits {
 // The bf16 attention on the tensor cores (paged_attn_tc.cu).
 sa_status paged_attn_tc(const void* Q, int64_t q_stride, const void* Kc, const void* Vc, const sa_paged_shape& s,
                         const paged::Params& p, float scale, void* O, const paged::Workspace& ws, cudaStream_t stream);
-uint32_t paged_tc_error_take();
 
 }  // namespace sa

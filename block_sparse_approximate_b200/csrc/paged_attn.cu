@@ -435,6 +435,8 @@ extern "C" sa_status sa_paged_attn_fwd(const void* Q, int64_t q_row_stride, cons
   sa_status r = check_attn_shape(shape, dtype, "sa_paged_attn_fwd");
   if (r != SA_OK) return r;
   if (window < 0) return fail(SA_ERR_INVALID_ARG, "sa_paged_attn_fwd: window must be 0 (none) or positive");
+  if (!(scale > 0.f && scale < INFINITY))
+    return fail(SA_ERR_INVALID_ARG, "sa_paged_attn_fwd: scale must be positive and finite");
   if (shape.T == 0 || shape.S == 0) return SA_OK;   // no row belongs to a request
   if (!Q || !q_start || !kv_len || !O || (shape.P > 0 && shape.max_pages > 0 && (!Kcache || !Vcache || !table)))
     return fail(SA_ERR_INVALID_ARG, "sa_paged_attn_fwd: Q, caches, q_start, kv_len, table and O are required");
@@ -458,7 +460,7 @@ extern "C" sa_status sa_paged_attn_fwd(const void* Q, int64_t q_row_stride, cons
            keys ? shape.max_pages : 0, window >= most ? 0 : window};
   Workspace ws;
   ws.desc = static_cast<Desc*>(workspace);
-  const bool tc = false;
+  const bool tc = dtype == SA_BF16;
   ws.rows_cap = rows_cap(shape, tc ? 256 : SimtTiling::BM);
   ws.ctas = tc ? Limits::kCtas : Limits::kCtasSimt;
   ws.o = reinterpret_cast<float*>(static_cast<char*>(workspace) + kDescBytes);
@@ -471,8 +473,7 @@ extern "C" sa_status sa_paged_attn_fwd(const void* Q, int64_t q_row_stride, cons
     return shape.d == 128 ? launch_combine<float, 128>(p, ws, O, st) : launch_combine<float, 64>(p, ws, O, st);
   }
   using bf = __nv_bfloat16;
-  r = shape.d == 128 ? launch_simt<bf, 128>(Q, q_row_stride, Kcache, Vcache, shape, p, scale, O, ws, st)
-                     : launch_simt<bf, 64>(Q, q_row_stride, Kcache, Vcache, shape, p, scale, O, ws, st);
+  r = paged_attn_tc(Q, q_row_stride, Kcache, Vcache, shape, p, scale, O, ws, st);
   if (r != SA_OK) return r;
   return shape.d == 128 ? launch_combine<bf, 128>(p, ws, O, st) : launch_combine<bf, 64>(p, ws, O, st);
 }

@@ -1,0 +1,702 @@
+// Attention of new tokens over a paged KV cache on the 5th-generation tensor
+// cores (tcgen05 + TMEM + TMA), bf16, d = 64 or 128.
+//
+// One persistent CTA per SM walks its share of the line of items (paged.cuh).
+// An item is up to 256 query rows (token-major, the query heads of one KV
+// head side by side), its keys come in tiles of 128, one TMA box per page and
+// 64 channels, so a tile may be gathered from 1 to 8 pages.
+//
+// Warp roles (384 threads):
+//   warps 0-3, 4-7  two softmax warpgroups ("streams").  Items of more than
+//              128 rows: stream s owns the rows 128 s .. 128 s + 127 and both
+//              use every key tile.  Items of up to 128 rows (decoding): both
+//              own the same rows, stream s takes the key tiles of its parity,
+//              and stream 0 merges the two states at the end.  So one
+//              group's softmax overlaps the other's MMAs in either case.
+//              Thread r of a group is query row r (TMEM lane r); warps
+//              without rows only keep the barriers' count;
+//   warp 8     TMA producer: K and V tiles into one ring of slots, the lanes
+//              share a tile's boxes;
+//   warp 9     MMA issuer: S = Q Kᵀ two steps ahead of O += P V (P read from
+//              TMEM, written over S), across item boundaries, so the next
+//              item's scores form during the epilogue;
+//   warp 10    loads the queries (any group size and row stride) into the
+//              swizzled layout with cp.async;
+//   warp 11    walks the share and hands the items to the others through a
+//              ring in shared memory.
+// TMEM (512 columns): S_0 [0,128), S_1 [128,256), O_0 [256,384), O_1 [384,512).
+//
+// Numerics: scores, maxima, sums and O in fp32; the weights are rounded to
+// bf16 for P V (their fp32 values enter the row sum), which moves an output
+// by at most 2^-8 Σ p|v| / Σ p, the size of the output's own rounding.
+//
+// Keys that a row does not see: the score is replaced by -inf, and as 0 · inf
+// is not 0, the values of an edge tile (one that some row of the item does
+// not see whole) are screened before P V: rows of V outside the item's span
+// are cleared, and elements that are not finite are cleared and added back
+// after the item's store for the rows that see them (add_unbounded).
+#include "paged.cuh"
+#include "tc_util.cuh"
+
+namespace sa {
+namespace {
+
+using namespace tc;
+using namespace paged;
+
+constexpr int kThreads = 384;
+// registers: 256 softmax threads x 208 + 128 others x 88 = 64512 = 384 x 168,
+// what the block is launched with (build.py checks ptxas reports 168)
+constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
+constexpr uint32_t kSpan = 128 * 128;          // 128 rows x one 128-byte swizzle span
+constexpr uint32_t kColO = 256;
+constexpr float kLazy = 8.0f;                  // O is rescaled when the maximum grew by more than 2^8
+constexpr uint32_t kExpFma = 0x49u;            // exponential pairs (of eight) on the FMA pipe
+constexpr int kItems = 4;                      // item ring
+
+struct TcTiling {
+  static constexpr int BM = 256, BN = 128;
+  // a tile of a two-tile item costs about two 128x128 steps of the tensor
+  // pipe, one of a half item its 64 KB from memory
+  static constexpr int kHalf = 128, kUnit = 4, kUnitHalf = 3, kOver = 6, kMinShare = 3;
+};
+
+struct TileItem {
+  int live, s, h, row0, r0, rv, p0, lo, hi, t0, n, slot, paired, qhalf, kt, pad;
+};
+static_assert(sizeof(TileItem) == 64, "item ring layout");
+
+template <int D>
+struct Lay {
+  static constexpr int NH = D / 64;
+  static constexpr uint32_t kTile = NH * kSpan;
+  static constexpr int NS = D == 128 ? 5 : 10;
+  static constexpr int B_QF = 0, B_QE = 2, B_KF = 4, B_KE = B_KF + NS, B_SF = B_KE + NS, B_PR = B_SF + 2,
+                       B_OD = B_PR + 2, B_OF = B_OD + 2, B_EX = B_OF + 2, B_IF = B_EX + 1, B_IE = B_IF + kItems,
+                       B_FIN = B_IE + kItems, NBAR = B_FIN + 1;
+  static constexpr uint32_t kRing = 2 * kTile;
+  static constexpr uint32_t kBarOff = kRing + NS * kTile;
+  static constexpr uint32_t kSlotOff = (kBarOff + 8 * NBAR + 15) / 16 * 16;  // tmem base, abort, unbounded
+  static constexpr uint32_t kItemOff = kSlotOff + 16;
+  static constexpr uint32_t kExOff = kItemOff + 64 * kItems;                 // stream 1's maxima and sums
+  static constexpr uint32_t kTotOff = kExOff;                                // lay_line's totals, before the roles
+  static constexpr uint32_t kEnd = kExOff + 2 * 128 * 4;
+  static constexpr size_t smem_bytes = 1024 + kEnd;
+};
+static_assert(Lay<128>::smem_bytes <= 232448 && Lay<64>::smem_bytes <= 232448, "shared memory of a CTA");
+static_assert(2 * Lay<64>::kTile >= kMaxRequests * sizeof(int64_t), "the line lies in the query tiles");
+
+__device__ __forceinline__ void mma_ss_w(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile("{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+               "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, {%5, %5, %5, %5}, p;\n\t}"
+               ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(0u) : "memory");
+}
+__device__ __forceinline__ void mma_ts_w(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile("{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+               "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, {%5, %5, %5, %5}, p;\n\t}"
+               ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(0u) : "memory");
+}
+__device__ __forceinline__ void mma_commit_w(uint32_t bar) {
+  asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+               "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
+               : "memory");
+}
+
+// A wait of a whole warp, bounded like mbar_wait.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
+}
+
+// The abort path's own wait: nothing can release it but the copy in flight.
+__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
+  const long long t0 = clock64();
+  for (;;) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (done || clock64() - t0 > kWaitCycles / 8) return;
+  }
+}
+
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+__device__ __forceinline__ float fmax3_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+__device__ __forceinline__ bool unbounded(uint32_t half) { return (half & 0x7f80u) == 0x7f80u; }
+
+// Whether some row of an item (first position p_first, keys below hi) does
+// not see the whole tile at k0.
+__device__ __forceinline__ bool edge_tile(int p_first, int hi, int window, int k0) {
+  return k0 + 127 > p_first || (window > 0 && k0 <= hi - 1 - window);
+}
+
+// Adds the values that are not finite, of the keys of edge tiles that a row
+// with last key `last` sees, to its stored output.  Runs only after such a
+// value was met in this CTA.
+template <typename T>
+__device__ __noinline__ void add_unbounded(const Params& p, int s, int h, int t0, int n, int p_first, int hi,
+                                           const __nv_bfloat16* Vc, int D, int last, T* dst) {
+  for (int t = 0; t < n; ++t) {
+    const int k0 = (t0 + t) * 128;
+    if (!edge_tile(p_first, hi, p.window, k0)) continue;
+    const int a = max(max(k0, 0), p.window > 0 ? last - p.window + 1 : 0), b = min(k0 + 127, last);
+    for (int key = a; key <= b; ++key) {
+      const int id = p.table[(size_t)s * p.max_pages + (key >> p.page_shift)];
+      if (id < 0 || id >= p.P) continue;
+      const int64_t row = (((int64_t)id * p.Hkv + h) << p.page_shift) + (key & ((1 << p.page_shift) - 1));
+      const __nv_bfloat16* v = Vc + row * D;
+      for (int e = 0; e < D; ++e) {
+        const float x = __bfloat162float(v[e]);
+        if (!(fabsf(x) < INFINITY)) dst[e] = from_f<T>(to_f(dst[e]) + x);
+      }
+    }
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                     const __nv_bfloat16* __restrict__ Q, int64_t q_stride, const __nv_bfloat16* __restrict__ Vc,
+                     const Params p, float scale2, __nv_bfloat16* __restrict__ O, const Workspace ws) {
+  pdl_wait();
+  pdl_trigger();
+  using L = Lay<D>;
+  using TL = TcTiling;
+  constexpr int NS = L::NS, NH = L::NH;
+  constexpr uint32_t kTile = L::kTile;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sb = smem_u32(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int c = blockIdx.x;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kSlotOff);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kSlotOff + 4);
+  volatile int* unbounded_flag = reinterpret_cast<volatile int*>(smem + L::kSlotOff + 8);
+  TileItem* items = reinterpret_cast<TileItem*>(smem + L::kItemOff);
+  auto bar = [&](int k) { return sb + L::kBarOff + 8u * k; };
+
+  // the line, in the memory of the query tiles (loaded after the first item is handed out)
+  int64_t* pre = reinterpret_cast<int64_t*>(smem);
+  const int64_t total = lay_line<TL, kThreads>(p, pre, reinterpret_cast<int64_t*>(smem + L::kTotOff));
+  const int parts = share_count<TL>(total, ws.ctas);
+  if (threadIdx.x == 0) ws.desc[c].valid = 0;
+  if (total == 0 || c >= parts) return;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(bar(L::B_QF + s), 32);
+      mbar_init(bar(L::B_QE + s), 1);
+      mbar_init(bar(L::B_SF + s), 1);
+      mbar_init(bar(L::B_PR + s), 4);
+      mbar_init(bar(L::B_OD + s), 1);
+      mbar_init(bar(L::B_OF + s), 4);
+    }
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(bar(L::B_KF + s), 1);
+      mbar_init(bar(L::B_KE + s), 1);
+    }
+    for (int s = 0; s < kItems; ++s) {
+      mbar_init(bar(L::B_IF + s), 1);
+      mbar_init(bar(L::B_IE + s), 11);         // producer, MMA issuer, query loader, 8 softmax warps
+    }
+    mbar_init(bar(L::B_EX), 4);
+    mbar_init(bar(L::B_FIN), 1);
+    *abort_flag = 0;
+    *unbounded_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 0) tmem_alloc(smem_u32(tmem_slot), 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = *tmem_slot;
+
+  // Item n of the ring: wait until it is handed out / give it back.
+  auto item_wait = [&](int n) { return warp_wait(bar(L::B_IF + n % kItems), (n / kItems) & 1, abort_flag); };
+  auto item_done = [&](int n) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(L::B_IE + n % kItems));
+  };
+
+  if (warp == 11) {
+    // ------------------------------------------------------------ walker
+    regs_dec<kOtherRegs>();
+    const int64_t w0 = share_start(total, parts, c), w1 = share_start(total, parts, c + 1);
+    Walker<TL> w;
+    w.find(p, pre, w0);
+    int n = 0, qhalf = 1, kt = 0;
+    for (bool more = true;;) {
+      int ta = 0, tb = 0;
+      bool got = false;
+      while (more && !got) {
+        if (w.start >= w1) more = false;
+        else if (!w.portion(w0, w1, ta, tb)) more = w.next(p);
+        else if (w.it.nt == 0) {
+          // no row of the item sees a key
+          for (int x = lane; x < w.it.rv * (D / 8); x += 32) {
+            const int r = w.it.r0 + x / (D / 8);
+            *reinterpret_cast<uint4*>(O + ((int64_t)(w.q.row0 + r / p.group) * p.Hq + w.h * p.group + r % p.group) * D +
+                                      8 * (x % (D / 8))) = make_uint4(0, 0, 0, 0);
+          }
+          more = w.next(p);
+        } else {
+          got = true;
+        }
+      }
+      if (n >= kItems && !warp_wait(bar(L::B_IE + n % kItems), ((n / kItems) - 1) & 1, abort_flag)) break;
+      const bool whole = ta == 0 && tb == w.it.nt;
+      const int slot = whole ? -1 : 2 * c + (n > 0);
+      const int paired = w.it.rv <= 128;
+      qhalf = paired ? 1 - qhalf : 1;          // half items alternate the two query tiles
+      if (lane == 0) {
+        items[n % kItems] = TileItem{got, w.s, w.h, w.q.row0, w.it.r0, w.it.rv, w.it.p0, w.it.lo, w.it.hi,
+                                     w.it.t0 + ta, tb - ta, slot, paired, qhalf, kt, 0};
+        if (got && !whole && ta == 0)
+          ws.desc[c] = Desc{w.start, total, parts, 1, slot, w.it.unit, w.it.nt, w.q.row0, w.it.r0, w.it.rv, w.h, 0};
+        mbar_arrive(bar(L::B_IF + n % kItems));
+      }
+      __syncwarp();
+      if (!got) break;
+      ++n;
+      kt += tb - ta;
+      more = w.next(p);
+    }
+  } else if (warp == 8) {
+    // ------------------------------------------------------------ producer
+    regs_dec<kOtherRegs>();
+    if (lane == 0) {
+      prefetch_tmap(&tmK);
+      prefetch_tmap(&tmV);
+    }
+    const int page = 1 << p.page_shift;
+    const int boxes = (128 >> p.page_shift) * NH;    // of a whole tile
+    const int pi = lane / NH, hf = lane % NH;
+    const uint32_t box_bytes = (uint32_t)page * 128u;
+    int seq = 0;                               // slots filled
+    bool ok = true;
+    for (int n = 0; ok; ++n) {
+      if (!item_wait(n)) break;
+      const TileItem it = items[n % kItems];
+      item_done(n);
+      if (!it.live) break;
+      for (int t = 0; ok && t < it.n; ++t) {
+        const int k0 = (it.t0 + t) * 128, key = k0 + pi * page;
+        const bool mine = lane < boxes && key < it.hi && key + page > it.lo;
+        int outer = p.P * p.Hkv;               // behind the pool: the box is filled with zeros
+        if (mine) {
+          const int id = p.table[(size_t)it.s * p.max_pages + (key >> p.page_shift)];
+          if (id >= 0 && id < p.P) outer = id * p.Hkv + it.h;
+        }
+        const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, mine)) * box_bytes;
+        for (int kv = 0; kv < 2; ++kv) {
+          const int s = seq % NS;
+          if (!warp_wait(bar(L::B_KE + s), ((seq / NS) & 1) ^ 1, abort_flag)) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) mbar_expect_tx(bar(L::B_KF + s), bytes);
+          __syncwarp();
+          if (mine)
+            tma_load_3d(sb + L::kRing + s * kTile + hf * kSpan + pi * box_bytes, kv ? &tmV : &tmK, 64 * hf, 0, outer,
+                        bar(L::B_KF + s));
+          ++seq;
+        }
+      }
+    }
+    if (*abort_flag)                           // let the loads in flight land before the CTA goes away
+      for (int q = seq > NS ? seq - NS : 0; q < seq; ++q) drain_wait(bar(L::B_KF + q % NS), (q / NS) & 1);
+  } else if (warp == 10) {
+    // ------------------------------------------------------------ query loader
+    regs_dec<kOtherRegs>();
+    constexpr int CH = D / 8, RI = 32 / CH;    // 16-byte chunks of a row, rows per warp instruction
+    const int ch = lane % CH, rr = lane / CH;
+    int loads = 0;                             // bit h: parity of the loads of query tile h
+    bool ok = true;
+    for (int n = 0; ok; ++n) {
+      if (!item_wait(n)) break;
+      const TileItem it = items[n % kItems];
+      item_done(n);
+      if (!it.live) break;
+      for (int hx = 0; hx < 2; ++hx) {
+        if (it.paired && hx != it.qhalf) continue;
+        const int first = it.paired ? 0 : 128 * hx;
+        const int rows = min(128, it.rv - first);
+        if (!warp_wait(bar(L::B_QE + hx), ((loads >> hx) & 1) ^ 1, abort_flag)) {
+          ok = false;
+          break;
+        }
+        loads ^= 1 << hx;
+        const uint32_t base = sb + hx * kTile + (ch >> 3) * kSpan;
+        const int row = it.r0 + first + rr;
+        int tok = row / p.group, head = row % p.group;
+        for (int r = rr; r < rows; r += RI) {
+          const __nv_bfloat16* src =
+              Q + (int64_t)(it.row0 + tok) * q_stride + (int64_t)(it.h * p.group + head) * D + 8 * ch;
+          const uint32_t dst = base + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+          for (head += RI; head >= p.group; head -= p.group) ++tok;
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        fence_async();
+        mbar_arrive(bar(L::B_QF + hx));
+      }
+    }
+  } else if (warp == 9) {
+    // ------------------------------------------------------------ MMA issuer
+    // Step x of an item belongs to stream x & 1: two steps per key tile, or
+    // one per tile (paired), with a dummy that makes their number even.
+    regs_dec<kOtherRegs>();
+    constexpr uint32_t idS = idesc_bf16_f32(128, 128, 0, 0);
+    constexpr uint32_t idO = idesc_bf16_f32(128, D, 0, 1);
+    // score cursor: step x of nx of item a, the K slot and its phase
+    int a = -1, x = 0, nx = 0, n_a = 0, paired_a = 0, qh_a = 0, ks = 0, kph = 0;
+    int qf = 0, pr = 0, drained = 0;           // bit h / st: parity of the barrier's next completion
+    bool end = false;
+    auto score_step = [&]() -> bool {          // false on abort; does nothing behind the last item
+      if (end) return true;
+      if (x == nx) {
+        ++a;
+        if (!item_wait(a)) return false;
+        const TileItem& it = items[a % kItems];
+        if (!it.live) {
+          end = true;
+          return true;
+        }
+        x = 0;
+        n_a = it.n;
+        paired_a = it.paired;
+        qh_a = it.qhalf;
+        nx = paired_a ? (n_a + 1) / 2 * 2 : 2 * n_a;
+      }
+      const int st = x & 1;
+      if (!paired_a || x < n_a) {
+        const int half = paired_a ? qh_a : st;
+        if (paired_a ? x == 0 : x < 2) {       // the first step on this query tile
+          if (!warp_wait(bar(L::B_QF + half), (qf >> half) & 1, abort_flag)) return false;
+          qf ^= 1 << half;
+        }
+        if (!warp_wait(bar(L::B_KF + ks), kph, abort_flag)) return false;
+        tc_fence_after();
+        const uint64_t qd = desc_sw128(sb + half * kTile, 16, 1024);
+        const uint64_t kd = desc_sw128(sb + L::kRing + ks * kTile, 16, 1024);
+        const uint32_t d = tbase + (uint32_t)st * 128;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t off = (k >> 2) * kSpan + (k & 3) * 32;
+          mma_ss_w(d, desc_adv(qd, off), desc_adv(kd, off), idS, k > 0);
+        }
+        mma_commit_w(bar(L::B_SF + st));
+        if (paired_a || st == 1) {             // the last use of this K tile
+          mma_commit_w(bar(L::B_KE + ks));
+          ks += 2;
+          if (ks >= NS) {
+            ks -= NS;
+            kph ^= 1;
+          }
+        }
+        if (paired_a ? x == n_a - 1 : x >= nx - 2) mma_commit_w(bar(L::B_QE + half));
+      }
+      ++x;
+      return true;
+    };
+    int vs = 1, vph = 0;
+    bool ok = score_step() && score_step();
+    for (int b = 0; ok; ++b) {
+      if (!item_wait(b)) break;
+      const int live = items[b % kItems].live, n_b = items[b % kItems].n, paired_b = items[b % kItems].paired;
+      if (!live) break;
+      const int real = paired_b ? n_b : 2 * n_b, ny = (real + 1) / 2 * 2;
+      for (int y = 0; y < ny; ++y) {
+        const int st = y & 1;
+        if (y < real) {
+          if (y < 2) {                         // this stream's O of an earlier item is read
+            if (!warp_wait(bar(L::B_OF + st), ((drained >> st) & 1) ^ 1, abort_flag)) { ok = false; break; }
+            drained ^= 1 << st;
+          }
+          if (!warp_wait(bar(L::B_PR + st), (pr >> st) & 1, abort_flag)) { ok = false; break; }
+          pr ^= 1 << st;
+          if (!warp_wait(bar(L::B_KF + vs), vph, abort_flag)) { ok = false; break; }
+          tc_fence_after();
+          const uint64_t vd = desc_sw128(sb + L::kRing + vs * kTile, kSpan, 1024);
+          const uint32_t pa = tbase + (uint32_t)st * 128, od = tbase + kColO + (uint32_t)st * 128;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) mma_ts_w(od, pa + k * 8, desc_adv(vd, k * 16 * 128), idO, (y >= 2 || k > 0));
+          if (paired_b || st == 1) {           // the last use of this V tile
+            mma_commit_w(bar(L::B_KE + vs));
+            vs += 2;
+            if (vs >= NS) {
+              vs -= NS;
+              vph ^= 1;
+            }
+          }
+          if (y + 2 >= real) mma_commit_w(bar(L::B_OD + st));   // the stream's last step of the item
+        }
+        // the scores overwrite this stream's P, whose product was issued before
+        if (!score_step()) { ok = false; break; }
+      }
+      item_done(b);
+    }
+    // every MMA issued above has completed before TMEM is released
+    mma_commit_w(bar(L::B_FIN));
+    drain_wait(bar(L::B_FIN), 0);
+  } else {
+    // ------------------------------------------------------------ softmax
+    regs_inc<kSoftmaxRegs>();
+    const int st = warp >> 2, wq = warp & 3, wr = wq * 32 + lane;
+    const uint32_t lrow = tbase + ((uint32_t)(wq * 32) << 16);
+    const uint32_t s_col = (uint32_t)st * 128, o_col = kColO + (uint32_t)st * 128;
+    float* ex = reinterpret_cast<float*>(smem + L::kExOff);   // [2][128]: stream 1's maxima, sums
+    int sf = 0, od = 0, exp_ = 0;              // parities of the next completions
+    bool ok = true;
+    for (int n = 0; ok; ++n) {
+      if (!item_wait(n)) break;
+      const TileItem it = items[n % kItems];
+      item_done(n);
+      if (!it.live) break;
+      const int rbase = it.paired ? 0 : st * 128, r = rbase + wr;
+      const bool live_warp = rbase + wq * 32 < it.rv;
+      const int last = it.p0 + (it.r0 + min(r, it.rv - 1)) / p.group;   // the row's last visible key
+      const int p_first = it.p0 + it.r0 / p.group;
+      const int U = it.paired ? (it.n - st + 1) / 2 : it.n;             // this stream's steps
+      float m_used = -INFINITY, l = 0.f;
+      for (int u = 0; u < U; ++u) {
+        const int t = it.paired ? 2 * u + st : u, k0 = (it.t0 + t) * 128;
+        // S is complete, and with it the product P V before it
+        if (!warp_wait(bar(L::B_SF + st), sf, abort_flag)) { ok = false; break; }
+        sf ^= 1;
+        const bool edge = edge_tile(p_first, it.hi, p.window, k0);
+        if (edge) {
+          // screen the V tile: thread wr takes row wr
+          const int seq = 2 * (it.kt + t) + 1, s = seq % NS;
+          if (!warp_wait(bar(L::B_KF + s), (seq / NS) & 1, abort_flag)) { ok = false; break; }
+          uint8_t* vrow = smem + L::kRing + s * kTile + wr * 128;
+          const bool out = k0 + wr < it.lo || k0 + wr >= it.hi;
+#pragma unroll
+          for (int j = 0; j < 8 * NH; ++j) {
+            uint4* q = reinterpret_cast<uint4*>(vrow + (j >> 3) * kSpan + (((j & 7) ^ (wr & 7)) << 4));
+            if (out) {
+              *q = make_uint4(0, 0, 0, 0);
+            } else {
+              uint4 y = *q;
+              uint32_t* w = reinterpret_cast<uint32_t*>(&y);
+              bool hit = false;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                if (unbounded(w[e])) { w[e] &= 0xffff0000u; hit = true; }
+                if (unbounded(w[e] >> 16)) { w[e] &= 0xffffu; hit = true; }
+              }
+              if (hit) {
+                *unbounded_flag = 1;           // before the values go
+                __threadfence_block();
+                *q = y;
+              }
+            }
+          }
+          fence_async();
+        }
+        if (live_warp) {
+          tc_fence_after();
+          uint32_t v[128];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            tmem_ld32(lrow + s_col + 32 * k, *reinterpret_cast<uint32_t(*)[32]>(&v[32 * k]));
+          tmem_wait_ld();
+          if (edge) {
+            const int hi = last - k0, lo = p.window > 0 ? last - p.window + 1 - k0 : 0;
+#pragma unroll
+            for (int e = 0; e < 128; ++e)
+              if (e > hi || e < lo) v[e] = __float_as_uint(-INFINITY);
+          }
+          float mx8[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) mx8[k] = -INFINITY;
+#pragma unroll
+          for (int e = 0; e < 64; ++e)
+            mx8[e & 7] = fmax3_nan(mx8[e & 7], __uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
+          const float mx = fmax3_nan(fmax3_nan(mx8[0], mx8[1], mx8[2]), fmax3_nan(mx8[3], mx8[4], mx8[5]),
+                                     fmax3_nan(mx8[6], mx8[7], mx8[7]));
+          // a score that is NaN or +inf makes the row NaN (as inf - inf does)
+          const float m_tile = mx < INFINITY ? mx * scale2 : NAN;
+          const bool need = !(m_tile <= m_used + kLazy);
+          float factor = 1.f;
+          if (need) {
+            factor = fast_exp2(m_used - m_tile);
+            m_used = m_tile;
+          }
+          // a masked score gives p = 0 or, on the FMA pipe, 2^-126; a row that
+          // has seen no key keeps such sums until the first key scales them by
+          // 0, or to the end, where its maximum of -inf drops them
+          const float ng = m_used == -INFINITY ? 0.f : -m_used;
+          float sm8[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) sm8[k] = 0.f;
+#pragma unroll
+          for (int e = 0; e < 64; ++e) {
+            float a0, a1, p0, p1;
+            ffma2(a0, a1, __uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]), scale2, scale2, ng, ng);
+            if ((kExpFma >> (e & 7)) & 1u) exp2_poly2(a0, a1, p0, p1);
+            else { p0 = fast_exp2(a0); p1 = fast_exp2(a1); }
+            fadd2(sm8[2 * (e & 3)], sm8[2 * (e & 3) + 1], p0, p1);
+            v[e] = pack_bf16(p0, p1);
+          }
+          l = l * factor + (((sm8[0] + sm8[1]) + (sm8[2] + sm8[3])) + ((sm8[4] + sm8[5]) + (sm8[6] + sm8[7])));
+          tmem_st32(lrow + s_col, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
+          tmem_st32(lrow + s_col + 32, *reinterpret_cast<uint32_t(*)[32]>(&v[32]));
+          if (u >= 1 && __any_sync(0xffffffffu, need)) {
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k) {
+              uint32_t o[32];
+              tmem_ld32(lrow + o_col + 32 * k, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * factor);
+              tmem_st32(lrow + o_col + 32 * k, o);
+            }
+          }
+          tmem_wait_st();
+          tc_fence_before();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(L::B_PR + st));
+      }
+      if (!ok) break;
+      if (U > 0) {
+        if (!warp_wait(bar(L::B_OD + st), od, abort_flag)) break;
+        od ^= 1;
+        tc_fence_after();
+      }
+      const int U1 = it.n / 2;                 // stream 1's steps of a paired item
+      if (it.paired && st == 1) {
+        // hand the state to stream 0 (which gives back O_1)
+        if (U > 0) {
+          ex[wr] = m_used;
+          ex[128 + wr] = l;
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(L::B_EX));
+        }
+        continue;
+      }
+      float f0 = 1.f, f1 = 0.f;
+      const bool merge = it.paired && U1 > 0;
+      if (merge) {
+        if (!warp_wait(bar(L::B_EX), exp_, abort_flag)) break;
+        exp_ ^= 1;
+        tc_fence_after();
+        const float m1 = ex[wr], l1 = ex[128 + wr];
+        const float M = m_used < m1 || m1 != m1 ? m1 : m_used;     // NaN if either is
+        const float base = M == -INFINITY ? 0.f : M;
+        f0 = fast_exp2(m_used - base);
+        f1 = fast_exp2(m1 - base);
+        l = l * f0 + l1 * f1;
+        m_used = M;
+      }
+      if (m_used == -INFINITY) l = 0.f;
+      const bool whole = it.slot < 0, mine = r < it.rv;
+      const float inv = !whole ? 1.f : (l > 0.f ? 1.0f / l : (l == 0.f ? 0.f : l));
+      const int rr = it.r0 + r;
+      __nv_bfloat16* orow = O + ((int64_t)(it.row0 + rr / p.group) * p.Hq + it.h * p.group + rr % p.group) * D;
+      const size_t at = (size_t)(whole ? 0 : it.slot) * ws.rows_cap + r;
+      if (live_warp) {
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k) {
+          uint32_t x[32], y[32];
+          tmem_ld32(lrow + o_col + 32 * k, x);
+          if (merge) tmem_ld32(lrow + kColO + 128 + 32 * k, y);
+          tmem_wait_ld();
+          float z[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            z[e] = __uint_as_float(x[e]) * f0;
+            if (merge) z[e] = fmaf(__uint_as_float(y[e]), f1, z[e]);
+            z[e] *= inv;
+          }
+          if (!mine) continue;
+          if (whole) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              reinterpret_cast<uint4*>(orow)[4 * k + q] =
+                  make_uint4(pack_bf16(z[8 * q], z[8 * q + 1]), pack_bf16(z[8 * q + 2], z[8 * q + 3]),
+                             pack_bf16(z[8 * q + 4], z[8 * q + 5]), pack_bf16(z[8 * q + 6], z[8 * q + 7]));
+          } else {
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              reinterpret_cast<float4*>(ws.o + at * D)[8 * k + q] =
+                  make_float4(z[4 * q], z[4 * q + 1], z[4 * q + 2], z[4 * q + 3]);
+          }
+        }
+        if (mine && !whole) *reinterpret_cast<float2*>(ws.ml + 2 * at) = make_float2(m_used, l);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (merge) mbar_arrive(bar(L::B_OF + 1));
+        mbar_arrive(bar(L::B_OF + st));
+      }
+      __threadfence_block();
+      if (*unbounded_flag && mine) {
+        if (whole) add_unbounded(p, it.s, it.h, it.t0, it.n, p_first, it.hi, Vc, D, last, orow);
+        else add_unbounded(p, it.s, it.h, it.t0, it.n, p_first, it.hi, Vc, D, last, ws.o + at * D);
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tbase, 512);
+  }
+}
+
+template <int D>
+sa_status launch(const CUtensorMap& mk, const CUtensorMap& mv, const void* Q, int64_t q_stride, const void* Vc,
+                 const Params& p, float scale, void* O, const Workspace& ws, cudaStream_t stream) {
+  auto kern = paged_attn_tc_kernel<D>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Lay<D>::smem_bytes) != cudaSuccess)
+    return launch_status("cudaFuncSetAttribute(paged_attn_tc_kernel)");
+  const cudaError_t le =
+      launch_pdl(kern, dim3(ws.ctas), dim3(kThreads), Lay<D>::smem_bytes, stream, mk, mv,
+                 static_cast<const __nv_bfloat16*>(Q), q_stride, static_cast<const __nv_bfloat16*>(Vc), p,
+                 scale * kLog2e, static_cast<__nv_bfloat16*>(O), ws);
+  if (le != cudaSuccess) return fail(SA_ERR_CUDA, std::string("paged_attn_tc_kernel: ") + cudaGetErrorString(le));
+  return launch_status("paged_attn_tc_kernel");
+}
+
+}  // namespace
+
+sa_status paged_attn_tc(const void* Q, int64_t q_stride, const void* Kc, const void* Vc, const sa_paged_shape& s,
+                        const paged::Params& p, float scale, void* O, const paged::Workspace& ws,
+                        cudaStream_t stream) {
+  CUtensorMap mk, mv;
+  uint64_t outer = (uint64_t)s.P * s.Hkv;
+  if (p.max_pages == 0) {
+    // no pages: every length reads as 0 and nothing is loaded through the maps
+    Kc = Vc = ws.o;
+    outer = 1;
+  }
+  if (!make_tmap_bf16_3d(&mk, Kc, s.d, s.page, outer, 64, s.page) ||
+      !make_tmap_bf16_3d(&mv, Vc, s.d, s.page, outer, 64, s.page))
+    return fail(SA_ERR_CUDA, "sa_paged_attn_fwd: cuTensorMapEncodeTiled failed for the caches");
+  return s.d == 128 ? launch<128>(mk, mv, Q, q_stride, Vc, p, scale, O, ws, stream)
+                    : launch<64>(mk, mv, Q, q_stride, Vc, p, scale, O, ws, stream);
+}
+
+uint32_t paged_tc_error_take() {
+  unsigned int v = 0, zero = 0;
+  if (cudaMemcpyFromSymbol(&v, tc::g_device_error, sizeof(v)) != cudaSuccess ||
+      cudaMemcpyToSymbol(tc::g_device_error, &zero, sizeof(zero)) != cudaSuccess)
+    return 0;
+  return v;
+}
+
+}  // namespace sa

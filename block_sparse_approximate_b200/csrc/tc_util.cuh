@@ -269,7 +269,8 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 }  // namespace tc
 
 // Host: builds a 3-D bf16 tensor map [outer][rows][cols] (cols innermost) with
-// a box of {64, 128, 1} and 128-byte swizzle.  Returns false on failure.
+// a box of {box_cols, box_rows, 1} and 128-byte swizzle.  Returns false on
+// failure.
 bool make_tmap_bf16_3d(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows, uint64_t outer,
                        uint32_t box_cols, uint32_t box_rows);
 

@@ -490,7 +490,8 @@ size_t sa_paged_attn_workspace_size(sa_paged_shape shape);
  * and sees the keys max(0, p - window + 1) .. p (window 0: from 0 on); query
  * head h reads KV head h / (Hq / Hkv):
  *   o = sum e^{scale q.k} v / sum e^{scale q.k}   over the keys it sees,
- * 0 for a row that sees none (kv_len[s] < n - i; a refused request).  One
+ * 0 for a row that sees none (kv_len[s] < n - i; a refused request).  scale
+ * is positive and finite.  One
  * row per request is decoding, several are a chunk of a prompt, and a call
  * may mix them.  Q: [T,Hq,d] with row stride q_row_stride (elements), the
  * heads of a row contiguous; O: [T,Hq,d] contiguous; rows from q_start[S] on

@@ -127,10 +127,10 @@ def test_attention_refusals(lib):
     ok = dict(S=4, T=8, Hq=8, Hkv=4, d=128, page=16, P=32, max_pages=4)
 
     def call(kw={}, Q=FAKE, qs=1024, Kc=FAKE, Vc=FAKE, dtype=1, q_start=FAKE, kv=FAKE, tab=FAKE, window=0, O=FAKE,
-             ws=FAKE, n=None):
+             ws=FAKE, n=None, scale=0.1):
         sh = bd.PagedShape(**{**ok, **kw})
         n = lib.sa_paged_attn_workspace_size(sh) if n is None else n
-        return f(Q, qs, Kc, Vc, dtype, sh, q_start, kv, tab, window, 0.1, O, ws, n, None)
+        return f(Q, qs, Kc, Vc, dtype, sh, q_start, kv, tab, window, scale, O, ws, n, None)
     assert call(dict(T=0)) == bd.SA_OK and call(dict(S=0)) == bd.SA_OK
     assert call(dict(Hq=6)) == bd.SA_ERR_INVALID_ARG
     assert call(dict(Hq=0)) == bd.SA_ERR_INVALID_ARG
@@ -140,6 +140,8 @@ def test_attention_refusals(lib):
     assert call(dict(T=1 << 28)) == bd.SA_ERR_UNSUPPORTED             # T * Hq rows
     assert call(dtype=7) == bd.SA_ERR_UNSUPPORTED
     assert call(window=-1) == bd.SA_ERR_INVALID_ARG
+    for scale in (0.0, -0.1, float("inf"), float("nan")):
+        assert call(scale=scale) == bd.SA_ERR_INVALID_ARG, scale
     for name in ("Q", "Kc", "Vc", "q_start", "kv", "tab", "O"):
         assert call(**{name: None}) == bd.SA_ERR_INVALID_ARG, name
     for name in ("Q", "Kc", "Vc", "O"):
