@@ -443,49 +443,60 @@ def sparse_attn_bwd_linear_mix(Q, K, V, O, dO, block_idx, block: int, alpha, sta
 
 
 # ---------------------------------------------------------------- paged KV cache
+# A serving step makes these calls with a few microseconds of GPU work each,
+# so the checks are kept to one attribute comparison apiece.
 
-def _paged_ptrs(dev, dtypes, names, tensors, contiguous=True):
-    """Pointers of tensors that must live on ``dev`` with the given dtypes."""
-    ptrs = []
-    for t, dt, n in zip(tensors, dtypes, names):
-        if t.device != dev or dev.type != "cuda":
-            raise ValueError(f"{n} must live on the call's CUDA device")
-        if t.dtype != dt:
-            raise ValueError(f"{n} must be {dt}, not {t.dtype}")
-        if contiguous and not t.is_contiguous():
-            raise ValueError(f"{n} must be contiguous")
-        ptrs.append(t.data_ptr())
-    return ptrs
+_I32, _I64, _U8 = torch.int32, torch.int64, torch.uint8
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _paged_ptr(t: torch.Tensor, i: int, dtype, name: str, dense: bool = True) -> int:
+    """Pointer of a tensor that must live on CUDA device ``i`` with ``dtype`` (and be contiguous)."""
+    if t.get_device() != i or t.dtype != dtype or (dense and not t.is_contiguous()):
+        if t.get_device() != i or i < 0:
+            raise ValueError(f"{name} must live on the call's CUDA device")
+        if t.dtype != dtype:
+            raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
 def _paged_rows(t: torch.Tensor, name: str) -> int:
     """The row stride (elements) of packed rows [T, heads, d] whose rows are dense."""
     T, H, d = t.shape
     s0, s1, s2 = t.stride()
-    if t.numel() and ((d > 1 and s2 != 1) or (H > 1 and s1 != d)):
+    if (s2 != 1 or (s1 != d and H > 1)) and t.numel():
         raise ValueError(f"{name}: the heads of a row must be contiguous (only the row stride is free)")
     return s0 if T > 1 else H * d
 
 
-def _paged_run(dev, stream, fn: str, *args):
-    """Calls the C entry point with ``dev`` current, on ``stream`` (default: the device's current stream)."""
-    s = (stream if stream is not None else torch.cuda.current_stream(dev)).cuda_stream
-    f = getattr(load(), fn)
-    if dev.index == torch.cuda.current_device():
+def _paged_call(i: int, stream, fn: str, f, *args):
+    """Calls the C entry point ``f`` with device ``i`` current, on ``stream`` (default: the device's current stream)."""
+    if i < 0:
+        raise ValueError(f"{fn}: tensors must live on a CUDA device")
+    if stream is not None:
+        s = stream.cuda_stream
+    elif _raw_stream is not None:
+        s = _raw_stream(i)
+    else:
+        s = torch.cuda.current_stream(i).cuda_stream
+    if i == torch.cuda.current_device():
         status = f(*args, s)
     else:
-        with torch.cuda.device(dev):
+        with torch.cuda.device(i):
             status = f(*args, s)
     if status != SA_OK:
         _check(fn, status)
 
 
-def _paged_empty(shape, dev, dtype, stream):
+def _paged_empty(shape, i: int, dtype, stream):
     """torch.empty on the stream that will use it, so that the caching allocator's reuse stays ordered with it."""
+    if i < 0:
+        raise ValueError("tensors must live on a CUDA device")
     if stream is None:
-        return torch.empty(shape, device=dev, dtype=dtype)
+        return torch.empty(shape, device=i, dtype=dtype)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, device=dev, dtype=dtype)
+        return torch.empty(shape, device=i, dtype=dtype)
 
 
 def paged_plan(ctx_len: torch.Tensor, new_len: torch.Tensor, held: torch.Tensor, table: torch.Tensor,
@@ -496,25 +507,24 @@ def paged_plan(ctx_len: torch.Tensor, new_len: torch.Tensor, held: torch.Tensor,
     and free_state [2] (all int32) in place and returns (q_start int32 [S+1],
     kv_len int32 [S], slots int64 [tokens]).  ``tokens``: rows of the step's
     packed arrays, padding included.  See sa_paged_plan for refused requests."""
-    dev = ctx_len.device
-    S, i32 = ctx_len.shape[0], torch.int32
-    if table.dim() != 2 or table.shape[0] != S or new_len.shape != (S,) or held.shape != (S,):
-        raise ValueError("new_len and held must be [S], table [S, max_pages]")
-    if free_state.shape != (2,) or free_pages.dim() != 1:
-        raise ValueError("free_state must be [2], free_pages [P]")
+    (S,), (P,), (rows, width) = ctx_len.shape, free_pages.shape, table.shape
+    if rows != S or new_len.shape != (S,) or held.shape != (S,) or free_state.shape != (2,):
+        raise ValueError("new_len and held must be [S], table [S, max_pages], free_state [2]")
+    i = ctx_len.get_device()
     if q_start is None:
-        q_start = _paged_empty((S + 1,), dev, i32, stream)
+        q_start = _paged_empty((S + 1,), i, _I32, stream)
     if kv_len is None:
-        kv_len = _paged_empty((S,), dev, i32, stream)
+        kv_len = _paged_empty((S,), i, _I32, stream)
     if slots is None:
-        slots = _paged_empty((tokens,), dev, torch.int64, stream)
+        slots = _paged_empty((tokens,), i, _I64, stream)
     if q_start.shape != (S + 1,) or kv_len.shape != (S,) or slots.shape != (tokens,):
         raise ValueError("q_start must be [S + 1], kv_len [S], slots [tokens]")
-    ptrs = _paged_ptrs(dev, (i32,) * 8 + (torch.int64,),
-                       ("ctx_len", "new_len", "held", "table", "free_pages", "free_state", "q_start", "kv_len", "slots"),
-                       (ctx_len, new_len, held, table, free_pages, free_state, q_start, kv_len, slots))
-    shape = PagedShape(S, tokens, 1, 1, 64, page, free_pages.shape[0], table.shape[1])
-    _paged_run(dev, stream, "sa_paged_plan", ptrs[0], ptrs[1], shape, *ptrs[2:])
+    ptr = _paged_ptr
+    _paged_call(i, stream, "sa_paged_plan", load().sa_paged_plan, ptr(ctx_len, i, _I32, "ctx_len"),
+                ptr(new_len, i, _I32, "new_len"), PagedShape(S, tokens, 1, 1, 64, page, P, width),
+                ptr(held, i, _I32, "held"), ptr(table, i, _I32, "table"), ptr(free_pages, i, _I32, "free_pages"),
+                ptr(free_state, i, _I32, "free_state"), ptr(q_start, i, _I32, "q_start"),
+                ptr(kv_len, i, _I32, "kv_len"), ptr(slots, i, _I64, "slots"))
     return q_start, kv_len, slots
 
 
@@ -522,15 +532,16 @@ def paged_append(K: torch.Tensor, V: torch.Tensor, slots: torch.Tensor, Kcache: 
                  stream=None) -> None:
     """Writes the rows K, V [T,Hkv,d] (views with a row stride serve) to their
     slots (int64 [T], negative: skipped) in the pools [P,Hkv,page,d]."""
-    dev, dt = Kcache.device, Kcache.dtype
     P, Hkv, page, d = Kcache.shape
-    T = K.shape[0]
-    if Vcache.shape != Kcache.shape or K.shape != (T, Hkv, d) or V.shape != (T, Hkv, d) or slots.shape != (T,):
+    rows = K.shape
+    T = rows[0]
+    if rows != (T, Hkv, d) or V.shape != rows or Vcache.shape != Kcache.shape or slots.shape != (T,):
         raise ValueError("K and V must be [T,Hkv,d], slots [T], the caches [P,Hkv,page,d]")
-    k, v = _paged_ptrs(dev, (dt, dt), ("K", "V"), (K, V), contiguous=False)
-    sl, kc, vc = _paged_ptrs(dev, (torch.int64, dt, dt), ("slots", "Kcache", "Vcache"), (slots, Kcache, Vcache))
-    _paged_run(dev, stream, "sa_paged_append", k, v, _paged_rows(K, "K"), _paged_rows(V, "V"), _dtype_code(Kcache),
-               PagedShape(0, T, Hkv, Hkv, d, page, P, 0), sl, kc, vc)
+    i, dt, ptr = Kcache.get_device(), Kcache.dtype, _paged_ptr
+    _paged_call(i, stream, "sa_paged_append", load().sa_paged_append, ptr(K, i, dt, "K", False),
+                ptr(V, i, dt, "V", False), _paged_rows(K, "K"), _paged_rows(V, "V"), _dtype_code(Kcache),
+                PagedShape(0, T, Hkv, Hkv, d, page, P, 0), ptr(slots, i, _I64, "slots"), ptr(Kcache, i, dt, "Kcache"),
+                ptr(Vcache, i, dt, "Vcache"))
 
 
 def paged_attn_workspace_size(S: int, T: int, Hq: int, Hkv: int, d: int, page: int, P: int, max_pages: int) -> int:
@@ -544,27 +555,23 @@ def paged_attn_fwd(Q: torch.Tensor, Kcache: torch.Tensor, Vcache: torch.Tensor, 
     rows Q [T,Hq,d] over their requests' pages; returns O [T,Hq,d], in which
     the rows from q_start[S] on are not written.  Chunks of prompts and
     single decoded tokens may share a call."""
-    dev, dt = Q.device, Q.dtype
     T, Hq, d = Q.shape
     P, Hkv, page, dc = Kcache.shape
-    S = kv_len.shape[0]
+    (S,), (rows, width) = kv_len.shape, table.shape
     if Vcache.shape != Kcache.shape or dc != d:
         raise ValueError("the caches must be [P,Hkv,page,d] with Q's d")
-    if table.dim() != 2 or table.shape[0] != S or q_start.shape != (S + 1,):
+    if rows != S or q_start.shape != (S + 1,):
         raise ValueError("q_start must be [S + 1], kv_len [S], table [S, max_pages]")
+    i, dt, ptr, lib = Q.get_device(), Q.dtype, _paged_ptr, load()
     if out is None:
-        out = _paged_empty((T, Hq, d), dev, dt, stream)
+        out = _paged_empty((T, Hq, d), i, dt, stream)
     elif out.shape != Q.shape:
         raise ValueError("out must have Q's shape")
-    shape = PagedShape(S, T, Hq, Hkv, d, page, P, table.shape[1])
+    shape = PagedShape(S, T, Hq, Hkv, d, page, P, width)
     if workspace is None:
-        need = int(load().sa_paged_attn_workspace_size(shape))
-        workspace = _paged_empty((max(need, 256),), dev, torch.uint8, stream)
-    (q,) = _paged_ptrs(dev, (dt,), ("Q",), (Q,), contiguous=False)
-    kc, vc, tab, qs, kl, o, ws = _paged_ptrs(
-        dev, (dt, dt, torch.int32, torch.int32, torch.int32, dt, torch.uint8),
-        ("Kcache", "Vcache", "table", "q_start", "kv_len", "out", "workspace"),
-        (Kcache, Vcache, table, q_start, kv_len, out, workspace))
-    _paged_run(dev, stream, "sa_paged_attn_fwd", q, _paged_rows(Q, "Q"), kc, vc, _dtype_code(Q), shape, qs, kl, tab,
-               int(window), float(scale), o, ws, workspace.numel())
+        workspace = _paged_empty((max(lib.sa_paged_attn_workspace_size(shape), 256),), i, _U8, stream)
+    _paged_call(i, stream, "sa_paged_attn_fwd", lib.sa_paged_attn_fwd, ptr(Q, i, dt, "Q", False), _paged_rows(Q, "Q"),
+                ptr(Kcache, i, dt, "Kcache"), ptr(Vcache, i, dt, "Vcache"), _dtype_code(Q), shape,
+                ptr(q_start, i, _I32, "q_start"), ptr(kv_len, i, _I32, "kv_len"), ptr(table, i, _I32, "table"),
+                window, scale, ptr(out, i, dt, "out"), ptr(workspace, i, _U8, "workspace"), workspace.numel())
     return out

@@ -41,7 +41,7 @@ def _headers():
 # attn_tc_kernel, attn_tc_linmix_kernel and paged_attn_tc_kernel reallocate
 # registers with setmaxnreg: their launch register count times 384 threads
 # must cover the split (256 x 216 + 128 x 40, and 128 x 216 + 128 x 96 +
-# 128 x 56, see attn_tc.cu; 256 x 208 + 128 x 88, see paged_attn_tc.cu), or
+# 128 x 56, see attn_tc.cu; 256 x 216 + 128 x 72, see paged_attn_tc.cu), or
 # setmaxnreg.inc would wait for registers that never come.
 TC_MIN_LAUNCH_REGS = {"attn_tc.cu": 158, "paged_attn_tc.cu": 168}
 

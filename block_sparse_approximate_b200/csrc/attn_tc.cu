@@ -1286,12 +1286,13 @@ htot_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
 }  // namespace
 
 bool make_tmap_bf16_3d(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows, uint64_t outer,
-                       uint32_t box_cols, uint32_t box_rows) {
+                       uint64_t row_stride, uint64_t outer_stride, uint32_t box_cols, uint32_t box_rows,
+                       uint32_t box_outer) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
   cuuint64_t dims[3] = {cols, rows, outer};
-  cuuint64_t strides[2] = {cols * 2, cols * rows * 2};
-  cuuint32_t box[3] = {box_cols, box_rows, 1};
+  cuuint64_t strides[2] = {row_stride * 2, outer_stride * 2};
+  cuuint32_t box[3] = {box_cols, box_rows, box_outer};
   cuuint32_t es[3] = {1, 1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,

@@ -7,9 +7,9 @@
 //
 // Work division of the attention.  The query rows of one (request, KV head)
 // are numbered token-major, r = token * group + (query head within the
-// group), so that a tile of BM consecutive rows shares its keys.  An item is
-// such a tile; its keys are the span its rows can see, walked in tiles of BN
-// keys.  The items of all requests are laid on one line, each as long as its
+// group), so that a tile of consecutive rows shares its keys.  An item is such
+// a tile (Params::bm rows); its keys are the span its rows can see, walked in
+// tiles of BN keys.  The items of all requests are laid on one line, each as long as its
 // cost, and the line is cut into equal shares, one per CTA: a share starts
 // and ends anywhere, also inside an item.  A CTA that holds all key tiles of
 // an item writes its output; otherwise each CTA writes a partial state
@@ -32,22 +32,43 @@ struct Params {
   const int32_t* table;     // [S][max_pages]
   int S, T, Hq, Hkv, group, page_shift, P, max_pages;
   int window;               // 0: none; else below max_pages * page
+  int bm, half;             // rows of an item; up to `half` rows are a half item
+};
+
+// Quotient of non-negative numbers; 32-bit division where both fit (a 64-bit
+// one costs a hundred instructions on the way to the first load).
+__host__ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  return ((a | b) >> 31) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
+// The line in equal shares: share c starts at c * each + min(c, rest).
+struct Shares {
+  int64_t each;
+  int32_t rest, parts;
+  __device__ __forceinline__ int64_t start(int c) const { return each * c + min(c, rest); }
 };
 
 // Partial states in the workspace: slot 2c holds the first item portion of
 // CTA c, slot 2c + 1 the last one.  desc[c] describes the split item whose
 // first key tile lies with CTA c.
 struct Desc {
-  int64_t start, total;     // the item's place on the line, the line's length
-  int32_t parts;            // shares of the line
-  int32_t valid, slot, unit, nt, row0, r0, rv, h, pad;
+  int64_t start;            // the item's place on the line
+  Shares shares;
+  int32_t valid, slot, unit, nt, row0, r0, rv, h;
 };
 
 struct Workspace {
   Desc* desc;               // [ctas]
-  float* o;                 // [2 ctas][rows_cap][d]
+  float* o;                 // [2 ctas][d / 4][rows_cap][4]: lanes of a warp hold rows, so stores coalesce
   float* ml;                // [2 ctas][rows_cap][2]: running maximum (log2 units), sum
   int rows_cap, ctas;
+  template <int D>
+  __device__ __forceinline__ float4* chunk(int slot, int k) const {   // columns 4k .. 4k + 3 of a slot's rows
+    return reinterpret_cast<float4*>(o) + ((size_t)slot * (D / 4) + k) * rows_cap;
+  }
+  __device__ __forceinline__ float2* state(int slot) const {
+    return reinterpret_cast<float2*>(ml) + (size_t)slot * rows_cap;
+  }
 };
 
 // ---- the items of a request
@@ -71,61 +92,77 @@ struct Item {
   int unit;          // cost of a tile
 };
 
-// A tiling is {BM rows, BN keys; up to kHalf rows cost kUnitHalf per tile
-// instead of kUnit; kOver is an item's own cost in the same unit; a share
-// holds at least kMinShare}.
+// A tiling has BN keys a tile; a tile costs kUnit, of a half item kUnitHalf;
+// kOver is an item's own cost in the same unit; a share holds at least
+// kMinShare.
 template <class TL>
-__device__ __forceinline__ Item item_of(const Request& q, int group, int window, int j) {
+__device__ __forceinline__ Item item_of(const Request& q, const Params& p, int j) {
   Item it;
-  it.r0 = j * TL::BM;
-  it.rv = min(TL::BM, q.n * group - it.r0);
+  it.r0 = j * p.bm;
+  it.rv = min(p.bm, q.n * p.group - it.r0);
   it.p0 = q.len - q.n;
-  const int p_lo = it.p0 + it.r0 / group, p_hi = it.p0 + (it.r0 + it.rv - 1) / group;
-  it.lo = window > 0 ? max(0, p_lo - window + 1) : 0;
+  const int p_lo = it.p0 + it.r0 / p.group, p_hi = it.p0 + (it.r0 + it.rv - 1) / p.group;
+  it.lo = p.window > 0 ? max(0, p_lo - p.window + 1) : 0;
   it.hi = max(0, p_hi + 1);
   it.t0 = it.lo / TL::BN;
   it.nt = it.hi > it.lo ? (it.hi + TL::BN - 1) / TL::BN - it.t0 : 0;
-  it.unit = it.rv <= TL::kHalf ? TL::kUnitHalf : TL::kUnit;
+  it.unit = it.rv <= p.half ? TL::kUnitHalf : TL::kUnit;
   return it;
 }
 template <class TL>
 __device__ __forceinline__ int item_cost(const Item& it) { return it.nt * it.unit + TL::kOver; }
-template <class TL>
-__device__ __forceinline__ int items_of(const Request& q, int group) { return (q.n * group + TL::BM - 1) / TL::BM; }
+__device__ __forceinline__ int items_of(const Request& q, const Params& p) {
+  return (q.n * p.group + p.bm - 1) / p.bm;
+}
 
-__device__ __forceinline__ int64_t share_start(int64_t total, int parts, int c) { return total * c / parts; }
+// Key tiles of an item that lie before the place x of its own stretch.
+__device__ __forceinline__ int tiles_before(int64_t x, int nt, int unit) {
+  return min(nt, (int)quotient(x, unit));
+}
+
 template <class TL>
-__device__ __forceinline__ int share_count(int64_t total, int ctas) {
-  const int64_t n = total / TL::kMinShare;
-  return (int)(n < 1 ? 1 : (n < ctas ? n : ctas));
+__device__ __forceinline__ Shares cut_line(int64_t total, int ctas) {
+  const int64_t n = quotient(total, TL::kMinShare);
+  Shares s;
+  s.parts = (int)(n < 1 ? 1 : (n < ctas ? n : ctas));
+  s.each = quotient(total, s.parts);
+  s.rest = (int)(total - s.each * s.parts);
+  return s;
 }
 
 // Lays the line: pre[s] = the end of request s on it (all threads of a block
 // of kThreads; pre and tot in shared memory).  Returns the line's length.
 template <class TL, int kThreads>
 __device__ int64_t lay_line(const Params& p, int64_t* pre, int64_t* tot) {
+  constexpr int NW = kThreads / 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int64_t run = 0;
+  // each request's cost; neighbours go to different warps, since requests of
+  // many items are taken by a whole warp, a lane an item
   for (int base = 0; base < p.S; base += kThreads) {
-    const int s = base + threadIdx.x;
+    const int s = base + lane * NW + warp;
     Request q{0, 0, 0};
     if (s < p.S) q = load_request(p, s);
-    const int nj = items_of<TL>(q, p.group);
+    const int nj = items_of(q, p);
     int64_t c = 0;
     if (nj <= 2)
-      for (int j = 0; j < nj; ++j) c += item_cost<TL>(item_of<TL>(q, p.group, p.window, j));
-    // requests of many items: the warp takes them one by one, a lane an item
+      for (int j = 0; j < nj; ++j) c += item_cost<TL>(item_of<TL>(q, p, j));
     for (unsigned big = __ballot_sync(0xffffffffu, nj > 2); big; big &= big - 1) {
       const int src = __ffs(big) - 1;
       const Request b{0, __shfl_sync(0xffffffffu, q.n, src), __shfl_sync(0xffffffffu, q.len, src)};
-      const int nb = items_of<TL>(b, p.group);
+      const int nb = items_of(b, p);
       int64_t sum = 0;
-      for (int j = lane; j < nb; j += 32) sum += item_cost<TL>(item_of<TL>(b, p.group, p.window, j));
+      for (int j = lane; j < nb; j += 32) sum += item_cost<TL>(item_of<TL>(b, p, j));
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
       if (lane == src) c = sum;
     }
-    c *= p.Hkv;
+    if (s < p.S) pre[s] = c * p.Hkv;
+  }
+  __syncthreads();
+  int64_t run = 0;
+  for (int base = 0; base < p.S; base += kThreads) {
+    const int s = base + threadIdx.x;
+    int64_t c = s < p.S ? pre[s] : 0;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int64_t y = __shfl_up_sync(0xffffffffu, c, o);
@@ -134,7 +171,8 @@ __device__ int64_t lay_line(const Params& p, int64_t* pre, int64_t* tot) {
     if (lane == 31) tot[warp] = c;
     __syncthreads();
     int64_t off = run, all = 0;
-    for (int w = 0; w < kThreads / 32; ++w) {
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
       if (w < warp) off += tot[w];
       all += tot[w];
     }
@@ -154,7 +192,7 @@ struct Walker {
   int64_t start;
 
   __device__ __forceinline__ void set_item(const Params& p) {
-    it = item_of<TL>(q, p.group, p.window, j);
+    it = item_of<TL>(q, p, j);
     cost = item_cost<TL>(it);
   }
   // The item that holds place w of the line, 0 <= w < its length.
@@ -168,13 +206,13 @@ struct Walker {
     }
     s = a;
     const int64_t first = s ? pre[s - 1] : 0;
-    const int64_t head = (pre[s] - first) / p.Hkv;
-    h = (int)((w - first) / head);
+    const int64_t head = quotient(pre[s] - first, p.Hkv);
+    h = (int)quotient(w - first, head);
     int64_t at = first + h * head;
     q = load_request(p, s);
-    nj = items_of<TL>(q, p.group);
+    nj = items_of(q, p);
     for (j = 0;; j += 32) {
-      const int mine = j + lane < nj ? item_cost<TL>(item_of<TL>(q, p.group, p.window, j + lane)) : 0;
+      const int mine = j + lane < nj ? item_cost<TL>(item_of<TL>(q, p, j + lane)) : 0;
       int64_t end = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -207,7 +245,7 @@ struct Walker {
           if (++s >= p.S) return false;
           q = load_request(p, s);
         } while (q.n == 0);
-        nj = items_of<TL>(q, p.group);
+        nj = items_of(q, p);
       }
     }
     set_item(p);
@@ -215,8 +253,8 @@ struct Walker {
   }
   // Key tiles [ta, tb) of the item in the share [w0, w1); false: none here.
   __device__ __forceinline__ bool portion(int64_t w0, int64_t w1, int& ta, int& tb) const {
-    ta = w0 > start ? min(it.nt, (int)((w0 - start) / it.unit)) : 0;
-    tb = w1 - start >= cost ? it.nt : min(it.nt, (int)((w1 - start) / it.unit));
+    ta = w0 > start ? tiles_before(w0 - start, it.nt, it.unit) : 0;
+    tb = tiles_before(w1 - start, it.nt, it.unit);
     return it.nt == 0 ? start >= w0 : ta < tb;
   }
 };

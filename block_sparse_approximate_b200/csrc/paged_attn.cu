@@ -20,32 +20,37 @@ using namespace paged;
 // its 16 tx lanes, in 32 bits as the products are.  Bound by the FMA pipe for
 // prompts; items of up to 16 rows (decode) form only the row group i = 0.
 constexpr int kSimtThreads = 256;
+constexpr int kSimtRows = 64;
 struct SimtTiling {
-  static constexpr int BM = 64, BN = 64;
-  // a tile of at most 16 rows costs its loads, about half a full tile
-  static constexpr int kHalf = 16, kUnit = 4, kUnitHalf = 2, kOver = 2, kMinShare = 4;
+  static constexpr int BN = 64;
+  // a tile of at most 16 rows (a half item here) costs its loads, about half a full tile
+  static constexpr int kUnit = 4, kUnitHalf = 2, kOver = 2, kMinShare = 4;
 };
 constexpr int kPitchP = 68;
 
-template <typename T>
-__device__ __forceinline__ float4 load4(const T* p);
-template <>
-__device__ __forceinline__ float4 load4<float>(const float* p) { return __ldg(reinterpret_cast<const float4*>(p)); }
-template <>
-__device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16* p) {
-  const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
-  const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.x));
-  const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.y));
-  return make_float4(a.x, a.y, b.x, b.y);
+__device__ __forceinline__ float4 load4(const float* p) { return __ldg(reinterpret_cast<const float4*>(p)); }
+__device__ __forceinline__ void store8(float* dst, const float* x, float f) {
+  reinterpret_cast<float4*>(dst)[0] = make_float4(x[0] * f, x[1] * f, x[2] * f, x[3] * f);
+  reinterpret_cast<float4*>(dst)[1] = make_float4(x[4] * f, x[5] * f, x[6] * f, x[7] * f);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* dst, const float* x, float f) {
+  uint4 u;
+  uint32_t* w = reinterpret_cast<uint32_t*>(&u);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * e] * f, x[2 * e + 1] * f);
+    w[e] = *reinterpret_cast<const uint32_t*>(&v);
+  }
+  *reinterpret_cast<uint4*>(dst) = u;
 }
 
 template <int D>
 constexpr size_t simt_smem() { return (size_t)(2 * 64 * (D + 4) + 64 * kPitchP) * 4; }
 
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kSimtThreads, 2)
-paged_attn_simt_kernel(const T* __restrict__ Q, int64_t q_stride, const T* __restrict__ Kc, const T* __restrict__ Vc,
-                       Params p, float scale2, T* __restrict__ O, Workspace ws) {
+paged_attn_simt_kernel(const float* __restrict__ Q, int64_t q_stride, const float* __restrict__ Kc,
+                       const float* __restrict__ Vc, Params p, float scale2, float* __restrict__ O, Workspace ws) {
   pdl_wait();
   pdl_trigger();
   using TL = SimtTiling;
@@ -55,8 +60,6 @@ paged_attn_simt_kernel(const T* __restrict__ Q, int64_t q_stride, const T* __res
   float* skv = sq + 64 * DP;
   float* sp = skv + 64 * DP;
   __shared__ int64_t tot[kSimtThreads / 32];
-  __shared__ int64_t share[2];
-  __shared__ int parts_s;
   struct Job {
     int live, s, h, row0, r0, rv, p0, lo, hi, t0, ta, tb, slot;   // slot < 0: the whole item
   };
@@ -67,17 +70,11 @@ paged_attn_simt_kernel(const T* __restrict__ Q, int64_t q_stride, const T* __res
   // the line, laid in the operand buffers before their first use
   int64_t* pre = reinterpret_cast<int64_t*>(smem_f);
   const int64_t total = lay_line<TL, kSimtThreads>(p, pre, tot);
-  const int parts = share_count<TL>(total, ws.ctas);
-  if (tid == 0) {
-    ws.desc[c].valid = 0;
-    share[0] = share_start(total, parts, c);
-    share[1] = share_start(total, parts, c + 1);
-    parts_s = parts;
-  }
-  if (total == 0 || c >= parts) return;
+  const Shares shares = cut_line<TL>(total, ws.ctas);
+  if (tid == 0) ws.desc[c].valid = 0;
+  if (total == 0 || c >= shares.parts) return;
   Walker<TL> w;
-  __syncthreads();
-  const int64_t w0 = share[0], w1 = share[1];
+  const int64_t w0 = shares.start(c), w1 = shares.start(c + 1);
   bool more = true;
   if (warp == 0) w.find(p, pre, w0);
   __syncthreads();                              // the line is read; its memory becomes the operands'
@@ -105,7 +102,7 @@ paged_attn_simt_kernel(const T* __restrict__ Q, int64_t q_stride, const T* __res
           const int slot = whole ? -1 : 2 * c + (emitted > 0);
           job = Job{1, w.s, w.h, w.q.row0, w.it.r0, w.it.rv, w.it.p0, w.it.lo, w.it.hi, w.it.t0, ta, tb, slot};
           if (!whole && ta == 0)
-            ws.desc[c] = Desc{w.start, total, parts_s, 1, slot, w.it.unit, w.it.nt, w.q.row0, w.it.r0, w.it.rv, w.h, 0};
+            ws.desc[c] = Desc{w.start, shares, 1, slot, w.it.unit, w.it.nt, w.q.row0, w.it.r0, w.it.rv, w.h};
         }
       }
       emitted += got;
@@ -137,7 +134,7 @@ paged_attn_simt_kernel(const T* __restrict__ Q, int64_t q_stride, const T* __res
       for (int k = 0; k < NC * 4; ++k) o[i][k] = 0.f;
     }
     const int mask = (1 << p.page_shift) - 1;
-    auto load_tile = [&](const T* cache, int k0) {
+    auto load_tile = [&](const float* cache, int k0) {
       for (int x = tid; x < 64 * (D / 4); x += kSimtThreads) {
         const int r = x / (D / 4), e = 4 * (x % (D / 4)), key = k0 + r;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -252,18 +249,17 @@ paged_attn_simt_kernel(const T* __restrict__ Q, int64_t q_stride, const T* __res
       const int rr = jb.r0 + r;
       if (jb.slot < 0) {
         const float inv = l[i] > 0.f ? 1.0f / l[i] : (l[i] == 0.f ? 0.f : l[i]);
-        T* dst = O + ((int64_t)(jb.row0 + rr / p.group) * p.Hq + jb.h * p.group + rr % p.group) * D + 4 * tx;
+        float* dst = O + ((int64_t)(jb.row0 + rr / p.group) * p.Hq + jb.h * p.group + rr % p.group) * D + 4 * tx;
 #pragma unroll
         for (int n = 0; n < NC; ++n)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) dst[64 * n + k] = from_f<T>(o[i][4 * n + k] * inv);
+          *reinterpret_cast<float4*>(dst + 64 * n) =
+              make_float4(o[i][4 * n] * inv, o[i][4 * n + 1] * inv, o[i][4 * n + 2] * inv, o[i][4 * n + 3] * inv);
       } else {
-        const size_t at = (size_t)jb.slot * ws.rows_cap + r;
 #pragma unroll
         for (int n = 0; n < NC; ++n)
-          *reinterpret_cast<float4*>(ws.o + at * D + 4 * tx + 64 * n) =
+          ws.chunk<D>(jb.slot, tx + 16 * n)[r] =
               make_float4(o[i][4 * n], o[i][4 * n + 1], o[i][4 * n + 2], o[i][4 * n + 3]);
-        if (tx == 0) *reinterpret_cast<float2*>(ws.ml + 2 * at) = make_float2(m[i], l[i]);
+        if (tx == 0) ws.state(jb.slot)[r] = make_float2(m[i], l[i]);
       }
     }
     __syncthreads();                            // job and queries are read
@@ -271,11 +267,12 @@ paged_attn_simt_kernel(const T* __restrict__ Q, int64_t q_stride, const T* __res
 }
 
 // ---------------------------------------------------------------- merge
-// Block (c, y) merges rows of the split item that starts in share c: the
-// states of its portions, in key order, so the result does not depend on
-// which CTA ran first.  Items of up to 8 portions: a warp a row; more: the
-// block's 8 warps take every 8th portion of a row each.  Reads a few hundred
-// KB; bound by latency.
+// Block (c, y) merges 16 columns of the split item that starts in share c:
+// the states of its portions, in a fixed order, so the result does not depend
+// on which CTA ran first.  A thread takes a row; items of few rows (decoding:
+// many portions) give each row several threads, every one of them the
+// portions of its residue, joined through shared memory.  Reads a few hundred
+// KB to some MB; bound by latency.
 constexpr int kCombineThreads = 256;
 
 template <typename T, int D>
@@ -283,27 +280,24 @@ __global__ void __launch_bounds__(kCombineThreads)
 paged_combine_kernel(Params p, Workspace ws, T* __restrict__ O) {
   pdl_wait();
   pdl_trigger();
-  constexpr int V = D / 32;
-  __shared__ int slots[2 * Limits::kCtasSimt];
+  __shared__ int slots[Limits::kCtasSimt + 1];
   __shared__ int count;
-  __shared__ float red[8][D + 2];
+  __shared__ float red[kCombineThreads][19];    // maximum, sum, 16 columns
   const Desc d = ws.desc[blockIdx.x];
   if (!d.valid) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // the portions' slots, in key order
   if (warp == 0) {
     const int64_t end_tiles = d.start + (int64_t)d.nt * d.unit;
     int n = 1;
     if (lane == 0) slots[0] = d.slot;
-    for (int base = blockIdx.x + 1; base < d.parts; base += 32) {
+    for (int base = blockIdx.x + 1; base < d.shares.parts; base += 32) {
       const int c = base + lane;
       bool in = false, over = true;
-      if (c < d.parts) {
-        const int64_t a = share_start(d.total, d.parts, c), b = share_start(d.total, d.parts, c + 1);
+      if (c < d.shares.parts) {
+        const int64_t a = d.shares.start(c), b = d.shares.start(c + 1);
         over = a >= end_tiles;
-        const int ta = (int)min((int64_t)d.nt, (a - d.start) / d.unit);
-        const int tb = (int)min((int64_t)d.nt, (b - d.start) / d.unit);
-        in = !over && ta < tb;
+        in = !over && tiles_before(a - d.start, d.nt, d.unit) < tiles_before(b - d.start, d.nt, d.unit);
       }
       const unsigned who = __ballot_sync(0xffffffffu, in);
       if (in) slots[n + __popc(who & ((1u << lane) - 1u))] = 2 * c;
@@ -314,57 +308,68 @@ paged_combine_kernel(Params p, Workspace ws, T* __restrict__ O) {
   }
   __syncthreads();
   const int n = count;
-  const bool by_warp = n <= 8;
-  const int step = by_warp ? 8 * gridDim.y : gridDim.y;
-  for (int r = by_warp ? blockIdx.y * 8 + warp : blockIdx.y; r < d.rv; r += step) {
-    float mx = -INFINITY;
-    for (int k = lane; k < n; k += 32) mx = fmaxf(mx, ws.ml[2 * ((size_t)slots[k] * ws.rows_cap + r)]);
-    mx = warp_max(mx);
-    const float base = mx == -INFINITY ? 0.f : mx;
-    float acc[V], sum = 0.f;
+  int rows = 16;                                // threads of a residue: a power of two over the rows
+  while (rows < d.rv) rows *= 2;
+  const int r = tid % rows, pl = tid / rows, step = kCombineThreads / rows;
+  const bool mine = r < d.rv;
+  float m = -INFINITY, sum = 0.f, acc[16];
 #pragma unroll
-    for (int e = 0; e < V; ++e) acc[e] = 0.f;
-#pragma unroll 4
-    for (int k = by_warp ? 0 : warp; k < n; k += by_warp ? 1 : 8) {
-      const size_t at = (size_t)slots[k] * ws.rows_cap + r;
-      const float2 ml = *reinterpret_cast<const float2*>(ws.ml + 2 * at);
-      const float f = fast_exp2(ml.x - base);
-      const float* src = ws.o + at * D + V * lane;
-      float x[V];
+  for (int e = 0; e < 16; ++e) acc[e] = 0.f;
+  if (mine) {
+    // NaN counts as the largest maximum: it belongs into the result
+    auto larger = [](float a, float b) { return a < b || b != b ? b : a; };
+    for (int k = pl; k < n; k += step) m = larger(m, ws.state(slots[k])[r].x);
+    const float base = m == -INFINITY ? 0.f : m;
+#pragma unroll 2
+    for (int k = pl; k < n; k += step) {
+      const float2 ml = ws.state(slots[k])[r];
+      float4 x[4];
 #pragma unroll
-      for (int e = 0; e < V; e += 2) {
-        const float2 y = *reinterpret_cast<const float2*>(src + e);
-        x[e] = y.x;
-        x[e + 1] = y.y;
-      }
+      for (int e = 0; e < 4; ++e) x[e] = ws.chunk<D>(slots[k], 4 * blockIdx.y + e)[r];
       if (ml.x == -INFINITY) continue;          // no visible key in this portion
+      const float f = fast_exp2(ml.x - base);
       sum = fmaf(ml.y, f, sum);
 #pragma unroll
-      for (int e = 0; e < V; ++e) acc[e] = fmaf(x[e], f, acc[e]);
-    }
-    if (!by_warp) {
-      __syncthreads();
-#pragma unroll
-      for (int e = 0; e < V; ++e) red[warp][V * lane + e] = acc[e];
-      if (lane == 0) red[warp][D] = sum;
-      __syncthreads();
-      if (warp > 0) continue;
-      sum = 0.f;
-#pragma unroll
-      for (int e = 0; e < V; ++e) acc[e] = 0.f;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        sum += red[k][D];
-#pragma unroll
-        for (int e = 0; e < V; ++e) acc[e] += red[k][V * lane + e];
+      for (int e = 0; e < 4; ++e) {
+        acc[4 * e] = fmaf(x[e].x, f, acc[4 * e]);
+        acc[4 * e + 1] = fmaf(x[e].y, f, acc[4 * e + 1]);
+        acc[4 * e + 2] = fmaf(x[e].z, f, acc[4 * e + 2]);
+        acc[4 * e + 3] = fmaf(x[e].w, f, acc[4 * e + 3]);
       }
     }
-    const float inv = sum > 0.f ? 1.0f / sum : (sum == 0.f ? 0.f : sum);
-    const int rr = d.r0 + r;
-    T* dst = O + ((int64_t)(d.row0 + rr / p.group) * p.Hq + d.h * p.group + rr % p.group) * D + V * lane;
+    if (step > 1) {
+      red[tid][0] = m;
+      red[tid][1] = sum;
 #pragma unroll
-    for (int e = 0; e < V; ++e) dst[e] = from_f<T>(acc[e] * inv);
+      for (int e = 0; e < 16; ++e) red[tid][2 + e] = acc[e];
+    }
   }
+  if (step > 1) {
+    __syncthreads();
+    if (pl > 0 || !mine) return;
+    float M = m;
+    for (int k = 1; k < step; ++k) M = M < red[tid + k * rows][0] || red[tid + k * rows][0] != red[tid + k * rows][0]
+                                           ? red[tid + k * rows][0] : M;
+    const float base = M == -INFINITY ? 0.f : M;
+    const float f0 = m == -INFINITY ? 0.f : fast_exp2(m - base);
+    sum *= f0;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) acc[e] *= f0;
+    for (int k = 1; k < step; ++k) {
+      const float* x = red[tid + k * rows];
+      if (x[0] == -INFINITY) continue;
+      const float f = fast_exp2(x[0] - base);
+      sum = fmaf(x[1], f, sum);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[e] = fmaf(x[2 + e], f, acc[e]);
+    }
+  }
+  if (!mine) return;
+  const float inv = sum > 0.f ? 1.0f / sum : (sum == 0.f ? 0.f : sum);
+  const int rr = d.r0 + r;
+  T* dst = O + ((int64_t)(d.row0 + rr / p.group) * p.Hq + d.h * p.group + rr % p.group) * D + 16 * blockIdx.y;
+#pragma unroll
+  for (int e = 0; e < 16; e += 8) store8(dst + e, acc + e, inv);
 }
 
 // ---------------------------------------------------------------- host side
@@ -379,30 +384,30 @@ constexpr size_t kDescBytes = (sizeof(Desc) * Limits::kCtasSimt + 255) / 256 * 2
 
 size_t workspace_bytes(const sa_paged_shape& s) {
   const size_t tc = (size_t)2 * Limits::kCtas * rows_cap(s, 256);
-  const size_t simt = (size_t)2 * Limits::kCtasSimt * rows_cap(s, SimtTiling::BM);
+  const size_t simt = (size_t)2 * Limits::kCtasSimt * rows_cap(s, kSimtRows);
   return kDescBytes + std::max(tc, simt) * (s.d + 2) * sizeof(float);
 }
 
-template <typename T, int D>
+template <int D>
 sa_status launch_simt(const void* Q, int64_t q_stride, const void* Kc, const void* Vc, const sa_paged_shape& s,
                       const Params& p, float scale, void* O, const Workspace& ws, cudaStream_t stream) {
   constexpr size_t smem = simt_smem<D>();
   static_assert(smem >= kMaxRequests * sizeof(int64_t), "the line lies in the operand buffers");
-  auto kern = paged_attn_simt_kernel<T, D>;
+  auto kern = paged_attn_simt_kernel<D>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return launch_status("cudaFuncSetAttribute(paged_attn_simt_kernel)");
   const cudaError_t le =
-      launch_pdl(kern, dim3(ws.ctas), dim3(kSimtThreads), smem, stream, static_cast<const T*>(Q), q_stride,
-                 static_cast<const T*>(Kc), static_cast<const T*>(Vc), p, scale * kLog2e, static_cast<T*>(O), ws);
+      launch_pdl(kern, dim3(ws.ctas), dim3(kSimtThreads), smem, stream, static_cast<const float*>(Q),
+                 q_stride, static_cast<const float*>(Kc), static_cast<const float*>(Vc), p, scale * kLog2e,
+                 static_cast<float*>(O), ws);
   if (le != cudaSuccess) return fail(SA_ERR_CUDA, std::string("paged_attn_simt_kernel: ") + cudaGetErrorString(le));
   return launch_status("paged_attn_simt_kernel");
 }
 
 template <typename T, int D>
 sa_status launch_combine(const Params& p, const Workspace& ws, void* O, cudaStream_t stream) {
-  const int y = std::max(1, std::min(32, ws.rows_cap / 8));
-  const cudaError_t le = launch_pdl(paged_combine_kernel<T, D>, dim3(ws.ctas, y), dim3(kCombineThreads), 0, stream, p,
-                                    ws, static_cast<T*>(O));
+  const cudaError_t le = launch_pdl(paged_combine_kernel<T, D>, dim3(ws.ctas, D / 16), dim3(kCombineThreads), 0,
+                                    stream, p, ws, static_cast<T*>(O));
   if (le != cudaSuccess) return fail(SA_ERR_CUDA, std::string("paged_combine_kernel: ") + cudaGetErrorString(le));
   return launch_status("paged_combine_kernel");
 }
@@ -440,6 +445,8 @@ extern "C" sa_status sa_paged_attn_fwd(const void* Q, int64_t q_row_stride, cons
   if (shape.T == 0 || shape.S == 0) return SA_OK;   // no row belongs to a request
   if (!Q || !q_start || !kv_len || !O || (shape.P > 0 && shape.max_pages > 0 && (!Kcache || !Vcache || !table)))
     return fail(SA_ERR_INVALID_ARG, "sa_paged_attn_fwd: Q, caches, q_start, kv_len, table and O are required");
+  if (dtype == SA_BF16 && shape.Hq / shape.Hkv > 128)
+    return fail(SA_ERR_UNSUPPORTED, "sa_paged_attn_fwd: at most 128 query heads per KV head in bf16");
   const int64_t e = (int64_t)dtype_size(dtype);
   if (shape.T > 1 && q_row_stride < (int64_t)shape.Hq * shape.d)
     return fail(SA_ERR_INVALID_ARG, "sa_paged_attn_fwd: q_row_stride is smaller than Hq * d");
@@ -456,19 +463,22 @@ extern "C" sa_status sa_paged_attn_fwd(const void* Q, int64_t q_row_stride, cons
   const bool keys = shape.P > 0 && shape.max_pages > 0;
   const int shift = 31 - __builtin_clz((unsigned)shape.page);
   const int most = keys ? shape.max_pages << shift : 0;
-  Params p{q_start, kv_len, table, shape.S, shape.T, shape.Hq, shape.Hkv, shape.Hq / shape.Hkv, shift, shape.P,
-           keys ? shape.max_pages : 0, window >= most ? 0 : window};
+  const bool tc = dtype == SA_BF16;
+  const int group = shape.Hq / shape.Hkv;
+  // tensor cores: 128-row tiles of whole tokens, two to an item
+  const int half = tc ? 128 / group * group : 16, bm = tc ? 2 * half : kSimtRows;
+  Params p{q_start, kv_len, table, shape.S, shape.T, shape.Hq, shape.Hkv, group, shift, shape.P,
+           keys ? shape.max_pages : 0, window >= most ? 0 : window, bm, half};
   Workspace ws;
   ws.desc = static_cast<Desc*>(workspace);
-  const bool tc = dtype == SA_BF16;
-  ws.rows_cap = rows_cap(shape, tc ? 256 : SimtTiling::BM);
+  ws.rows_cap = rows_cap(shape, tc ? 256 : kSimtRows);
   ws.ctas = tc ? Limits::kCtas : Limits::kCtasSimt;
   ws.o = reinterpret_cast<float*>(static_cast<char*>(workspace) + kDescBytes);
   ws.ml = ws.o + (size_t)2 * ws.ctas * ws.rows_cap * shape.d;
   cudaStream_t st = as_stream(stream);
   if (dtype == SA_FP32) {
-    r = shape.d == 128 ? launch_simt<float, 128>(Q, q_row_stride, Kcache, Vcache, shape, p, scale, O, ws, st)
-                       : launch_simt<float, 64>(Q, q_row_stride, Kcache, Vcache, shape, p, scale, O, ws, st);
+    r = shape.d == 128 ? launch_simt<128>(Q, q_row_stride, Kcache, Vcache, shape, p, scale, O, ws, st)
+                       : launch_simt<64>(Q, q_row_stride, Kcache, Vcache, shape, p, scale, O, ws, st);
     if (r != SA_OK) return r;
     return shape.d == 128 ? launch_combine<float, 128>(p, ws, O, st) : launch_combine<float, 64>(p, ws, O, st);
   }

@@ -2,16 +2,17 @@
 // cores (tcgen05 + TMEM + TMA), bf16, d = 64 or 128.
 //
 // One persistent CTA per SM walks its share of the line of items (paged.cuh).
-// An item is up to 256 query rows (token-major, the query heads of one KV
-// head side by side), its keys come in tiles of 128, one TMA box per page and
-// 64 channels, so a tile may be gathered from 1 to 8 pages.
+// An item is up to two tiles of query rows (token-major, the query heads of
+// one KV head side by side; a tile holds as many whole tokens as fit 128 rows,
+// so that a TMA box of tokens x heads x 64 channels loads it whatever the group
+// size).  Its keys come in tiles of 128, one box per page and 64 channels, so a
+// key tile may be gathered from 1 to 8 pages.
 //
 // Warp roles (384 threads):
-//   warps 0-3, 4-7  two softmax warpgroups ("streams").  Items of more than
-//              128 rows: stream s owns the rows 128 s .. 128 s + 127 and both
-//              use every key tile.  Items of up to 128 rows (decoding): both
-//              own the same rows, stream s takes the key tiles of its parity,
-//              and stream 0 merges the two states at the end.  So one
+//   warps 0-3, 4-7  two softmax warpgroups ("streams").  Items of two row
+//              tiles: stream s owns tile s and both use every key tile.  Items
+//              of one row tile (decoding): both own it, stream s takes the key
+//              tiles of its parity, and stream 0 merges the two states.  So one
 //              group's softmax overlaps the other's MMAs in either case.
 //              Thread r of a group is query row r (TMEM lane r); warps
 //              without rows only keep the barriers' count;
@@ -20,8 +21,7 @@
 //   warp 9     MMA issuer: S = Q Kᵀ two steps ahead of O += P V (P read from
 //              TMEM, written over S), across item boundaries, so the next
 //              item's scores form during the epilogue;
-//   warp 10    loads the queries (any group size and row stride) into the
-//              swizzled layout with cp.async;
+//   warp 10    loads the query tiles (TMA);
 //   warp 11    walks the share and hands the items to the others through a
 //              ring in shared memory.
 // TMEM (512 columns): S_0 [0,128), S_1 [128,256), O_0 [256,384), O_1 [384,512).
@@ -45,9 +45,9 @@ using namespace tc;
 using namespace paged;
 
 constexpr int kThreads = 384;
-// registers: 256 softmax threads x 208 + 128 others x 88 = 64512 = 384 x 168,
+// registers: 256 softmax threads x 216 + 128 others x 72 = 64512 = 384 x 168,
 // what the block is launched with (build.py checks ptxas reports 168)
-constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
+constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
 constexpr uint32_t kSpan = 128 * 128;          // 128 rows x one 128-byte swizzle span
 constexpr uint32_t kColO = 256;
 constexpr float kLazy = 8.0f;                  // O is rescaled when the maximum grew by more than 2^8
@@ -55,10 +55,10 @@ constexpr uint32_t kExpFma = 0x49u;            // exponential pairs (of eight) o
 constexpr int kItems = 4;                      // item ring
 
 struct TcTiling {
-  static constexpr int BM = 256, BN = 128;
-  // a tile of a two-tile item costs about two 128x128 steps of the tensor
+  static constexpr int BN = 128;
+  // a key tile of a two-tile item costs about two 128x128 steps of the tensor
   // pipe, one of a half item its 64 KB from memory
-  static constexpr int kHalf = 128, kUnit = 4, kUnitHalf = 3, kOver = 6, kMinShare = 3;
+  static constexpr int kUnit = 4, kUnitHalf = 3, kOver = 6, kMinShare = 3;
 };
 
 struct TileItem {
@@ -86,15 +86,48 @@ struct Lay {
 static_assert(Lay<128>::smem_bytes <= 232448 && Lay<64>::smem_bytes <= 232448, "shared memory of a CTA");
 static_assert(2 * Lay<64>::kTile >= kMaxRequests * sizeof(int64_t), "the line lies in the query tiles");
 
-__device__ __forceinline__ void mma_ss_w(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile("{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-               "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, {%5, %5, %5, %5}, p;\n\t}"
-               ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(0u) : "memory");
+// The MMAs of one step in one asm block: the converged warp elects a lane
+// once and that lane issues them back to back, the operands' descriptors
+// advanced by constants (only the start-address field changes, and no carry
+// leaves it).  With an election and a descriptor per MMA the issuing warp,
+// which shares its scheduler with two softmax warps, was the slowest role of
+// the kernel (2700 cycles a step, 1100 of them here).
+
+// S(tmem) = A · B, both K-major tiles of 64-channel spans 16 KB apart.
+template <int D>
+__device__ __forceinline__ void mma_scores(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
+#define SA_STEP(OFF, ACC)                                                                  \
+  "add.s64 ra, %1, " #OFF ";\n\tadd.s64 rb, %2, " #OFF ";\n\t"                             \
+  "@e tcgen05.mma.cta_group::1.kind::f16 [%0], ra, rb, %3, {%4, %4, %4, %4}, " #ACC ";\n\t"
+  if constexpr (D == 128) {
+    asm volatile(
+        "{\n\t.reg .pred e, f, t;\n\t.reg .b64 ra, rb;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 f, %4, 0;\n\tsetp.eq.b32 t, %4, 0;\n\t"
+        SA_STEP(0, f) SA_STEP(2, t) SA_STEP(4, t) SA_STEP(6, t)
+        SA_STEP(1024, t) SA_STEP(1026, t) SA_STEP(1028, t) SA_STEP(1030, t) "}"
+        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(0u) : "memory");
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred e, f, t;\n\t.reg .b64 ra, rb;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 f, %4, 0;\n\tsetp.eq.b32 t, %4, 0;\n\t"
+        SA_STEP(0, f) SA_STEP(2, t) SA_STEP(4, t) SA_STEP(6, t) "}"
+        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(0u) : "memory");
+  }
+#undef SA_STEP
 }
-__device__ __forceinline__ void mma_ts_w(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile("{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-               "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, {%5, %5, %5, %5}, p;\n\t}"
-               ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(0u) : "memory");
+
+// O(tmem) (+)= P(tmem) · V, V an MN-major tile of 128 rows: 16 keys a step.
+__device__ __forceinline__ void mma_values(uint32_t d, uint32_t pa, uint64_t v, uint32_t idesc, uint32_t accumulate) {
+#define SA_STEP(COL, OFF, ACC)                                                             \
+  "add.s32 rp, %1, " #COL ";\n\tadd.s64 rv, %2, " #OFF ";\n\t"                             \
+  "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [rp], rv, %3, {%5, %5, %5, %5}, " #ACC ";\n\t"
+  asm volatile(
+      "{\n\t.reg .pred e, f, t;\n\t.reg .b64 rv;\n\t.reg .b32 rp;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 f, %4, 0;\n\tsetp.eq.b32 t, %5, 0;\n\t"
+      SA_STEP(0, 0, f) SA_STEP(8, 128, t) SA_STEP(16, 256, t) SA_STEP(24, 384, t)
+      SA_STEP(32, 512, t) SA_STEP(40, 640, t) SA_STEP(48, 768, t) SA_STEP(56, 896, t) "}"
+      ::"r"(d), "r"(pa), "l"(v), "r"(idesc), "r"(accumulate), "r"(0u) : "memory");
+#undef SA_STEP
 }
 __device__ __forceinline__ void mma_commit_w(uint32_t bar) {
   asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
@@ -102,24 +135,34 @@ __device__ __forceinline__ void mma_commit_w(uint32_t bar) {
                : "memory");
 }
 
-// A wait of a whole warp, bounded like mbar_wait.
+__device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+
+// A wait of a whole warp, bounded like mbar_wait.  The first try is kept
+// short: most waits of the MMA issuer find their barrier complete.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
+  if (__all_sync(0xffffffffu, try_wait(bar, parity))) return true;
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
 }
+
+// A value that all lanes of the warp hold, in a form that the compiler knows
+// to be uniform (the MMA operands then live in uniform registers).
+template <typename T>
+__device__ __forceinline__ T uniform(T x) { return __shfl_sync(0xffffffffu, x, 0); }
 
 // The abort path's own wait: nothing can release it but the copy in flight.
 __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity) {
   const long long t0 = clock64();
-  for (;;) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    if (done || clock64() - t0 > kWaitCycles / 8) return;
+  while (!try_wait(bar, parity) && clock64() - t0 < kWaitCycles / 8) {
   }
 }
 
@@ -140,11 +183,11 @@ __device__ __forceinline__ bool edge_tile(int p_first, int hi, int window, int k
 }
 
 // Adds the values that are not finite, of the keys of edge tiles that a row
-// with last key `last` sees, to its stored output.  Runs only after such a
-// value was met in this CTA.
+// with last key `last` sees, to its stored output (groups of four columns
+// `stride` elements apart).  Runs only after such a value was met in this CTA.
 template <typename T>
 __device__ __noinline__ void add_unbounded(const Params& p, int s, int h, int t0, int n, int p_first, int hi,
-                                           const __nv_bfloat16* Vc, int D, int last, T* dst) {
+                                           const __nv_bfloat16* Vc, int D, int last, T* dst, int stride) {
   for (int t = 0; t < n; ++t) {
     const int k0 = (t0 + t) * 128;
     if (!edge_tile(p_first, hi, p.window, k0)) continue;
@@ -156,17 +199,34 @@ __device__ __noinline__ void add_unbounded(const Params& p, int s, int h, int t0
       const __nv_bfloat16* v = Vc + row * D;
       for (int e = 0; e < D; ++e) {
         const float x = __bfloat162float(v[e]);
-        if (!(fabsf(x) < INFINITY)) dst[e] = from_f<T>(to_f(dst[e]) + x);
+        T* o = dst + (size_t)(e >> 2) * stride + (e & 3);
+        if (!(fabsf(x) < INFINITY)) *o = from_f<T>(to_f(*o) + x);
       }
     }
   }
 }
 
+// 64 bytes of a lane's own row; with 32-byte stores where the rows allow them,
+// whole sectors, half the passes of 16-byte ones.
+__device__ __forceinline__ void store64(void* dst, const uint32_t (&u)[16], bool wide) {
+  if (wide) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                   ::"l"(static_cast<char*>(dst) + 32 * k), "r"(u[8 * k]), "r"(u[8 * k + 1]), "r"(u[8 * k + 2]),
+                     "r"(u[8 * k + 3]), "r"(u[8 * k + 4]), "r"(u[8 * k + 5]), "r"(u[8 * k + 6]), "r"(u[8 * k + 7])
+                   : "memory");
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      static_cast<uint4*>(dst)[k] = make_uint4(u[4 * k], u[4 * k + 1], u[4 * k + 2], u[4 * k + 3]);
+  }
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                     const __nv_bfloat16* __restrict__ Q, int64_t q_stride, const __nv_bfloat16* __restrict__ Vc,
-                     const Params p, float scale2, __nv_bfloat16* __restrict__ O, const Workspace ws) {
+paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                     const __grid_constant__ CUtensorMap tmV, const __nv_bfloat16* __restrict__ Vc, const Params p, float scale2, __nv_bfloat16* __restrict__ O, const Workspace ws) {
   pdl_wait();
   pdl_trigger();
   using L = Lay<D>;
@@ -176,7 +236,10 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sb = smem_u32(smem);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // hardware warps 0-3 are the roles 8-11 and come first: the scheduler prefers
+  // older warps, and the MMA issuer must not wait behind the softmax (1.5% of
+  // the kernel)
+  const int hw = uniform((int)(threadIdx.x >> 5)), warp = hw < 4 ? hw + 8 : hw - 4, lane = threadIdx.x & 31;
   const int c = blockIdx.x;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kSlotOff);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kSlotOff + 4);
@@ -187,13 +250,13 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
   // the line, in the memory of the query tiles (loaded after the first item is handed out)
   int64_t* pre = reinterpret_cast<int64_t*>(smem);
   const int64_t total = lay_line<TL, kThreads>(p, pre, reinterpret_cast<int64_t*>(smem + L::kTotOff));
-  const int parts = share_count<TL>(total, ws.ctas);
+  const Shares shares = cut_line<TL>(total, ws.ctas);
   if (threadIdx.x == 0) ws.desc[c].valid = 0;
-  if (total == 0 || c >= parts) return;
+  if (total == 0 || c >= shares.parts) return;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2; ++s) {
-      mbar_init(bar(L::B_QF + s), 32);
+      mbar_init(bar(L::B_QF + s), 1);
       mbar_init(bar(L::B_QE + s), 1);
       mbar_init(bar(L::B_SF + s), 1);
       mbar_init(bar(L::B_PR + s), 4);
@@ -218,7 +281,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tbase = *tmem_slot;
+  const uint32_t tbase = uniform(*tmem_slot);
 
   // Item n of the ring: wait until it is handed out / give it back.
   auto item_wait = [&](int n) { return warp_wait(bar(L::B_IF + n % kItems), (n / kItems) & 1, abort_flag); };
@@ -230,7 +293,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
   if (warp == 11) {
     // ------------------------------------------------------------ walker
     regs_dec<kOtherRegs>();
-    const int64_t w0 = share_start(total, parts, c), w1 = share_start(total, parts, c + 1);
+    const int64_t w0 = shares.start(c), w1 = shares.start(c + 1);
     Walker<TL> w;
     w.find(p, pre, w0);
     int n = 0, qhalf = 1, kt = 0;
@@ -255,13 +318,13 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
       if (n >= kItems && !warp_wait(bar(L::B_IE + n % kItems), ((n / kItems) - 1) & 1, abort_flag)) break;
       const bool whole = ta == 0 && tb == w.it.nt;
       const int slot = whole ? -1 : 2 * c + (n > 0);
-      const int paired = w.it.rv <= 128;
+      const int paired = w.it.rv <= p.half;
       qhalf = paired ? 1 - qhalf : 1;          // half items alternate the two query tiles
       if (lane == 0) {
         items[n % kItems] = TileItem{got, w.s, w.h, w.q.row0, w.it.r0, w.it.rv, w.it.p0, w.it.lo, w.it.hi,
                                      w.it.t0 + ta, tb - ta, slot, paired, qhalf, kt, 0};
         if (got && !whole && ta == 0)
-          ws.desc[c] = Desc{w.start, total, parts, 1, slot, w.it.unit, w.it.nt, w.q.row0, w.it.r0, w.it.rv, w.h, 0};
+          ws.desc[c] = Desc{w.start, shares, 1, slot, w.it.unit, w.it.nt, w.q.row0, w.it.r0, w.it.rv, w.h};
         mbar_arrive(bar(L::B_IF + n % kItems));
       }
       __syncwarp();
@@ -317,8 +380,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
   } else if (warp == 10) {
     // ------------------------------------------------------------ query loader
     regs_dec<kOtherRegs>();
-    constexpr int CH = D / 8, RI = 32 / CH;    // 16-byte chunks of a row, rows per warp instruction
-    const int ch = lane % CH, rr = lane / CH;
+    if (lane == 0) prefetch_tmap(&tmQ);
     int loads = 0;                             // bit h: parity of the loads of query tile h
     bool ok = true;
     for (int n = 0; ok; ++n) {
@@ -326,30 +388,28 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
       const TileItem it = items[n % kItems];
       item_done(n);
       if (!it.live) break;
+      const int tok = it.row0 + it.r0 / p.group;
       for (int hx = 0; hx < 2; ++hx) {
         if (it.paired && hx != it.qhalf) continue;
-        const int first = it.paired ? 0 : 128 * hx;
-        const int rows = min(128, it.rv - first);
         if (!warp_wait(bar(L::B_QE + hx), ((loads >> hx) & 1) ^ 1, abort_flag)) {
           ok = false;
           break;
         }
         loads ^= 1 << hx;
-        const uint32_t base = sb + hx * kTile + (ch >> 3) * kSpan;
-        const int row = it.r0 + first + rr;
-        int tok = row / p.group, head = row % p.group;
-        for (int r = rr; r < rows; r += RI) {
-          const __nv_bfloat16* src =
-              Q + (int64_t)(it.row0 + tok) * q_stride + (int64_t)(it.h * p.group + head) * D + 8 * ch;
-          const uint32_t dst = base + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-          for (head += RI; head >= p.group; head -= p.group) ++tok;
+        // rows of other requests behind this one's may come along: a row of S
+        // depends on its own row of Q alone, and they are not stored
+        if (lane == 0) {
+          mbar_expect_tx(bar(L::B_QF + hx), (uint32_t)(p.half * D * 2));
+#pragma unroll
+          for (int hf = 0; hf < NH; ++hf)
+            tma_load_3d(sb + hx * kTile + hf * kSpan, &tmQ, 64 * hf, it.h * p.group,
+                        tok + (it.paired ? 0 : hx * (p.half / p.group)), bar(L::B_QF + hx));
         }
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        fence_async();
-        mbar_arrive(bar(L::B_QF + hx));
+        __syncwarp();
       }
     }
+    if (*abort_flag)                           // a completed load's wait returns at once
+      for (int hx = 0; hx < 2; ++hx) drain_wait(bar(L::B_QF + hx), ((loads >> hx) & 1) ^ 1);
   } else if (warp == 9) {
     // ------------------------------------------------------------ MMA issuer
     // Step x of an item belongs to stream x & 1: two steps per key tile, or
@@ -367,14 +427,14 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
         ++a;
         if (!item_wait(a)) return false;
         const TileItem& it = items[a % kItems];
-        if (!it.live) {
+        if (!uniform(it.live)) {
           end = true;
           return true;
         }
         x = 0;
-        n_a = it.n;
-        paired_a = it.paired;
-        qh_a = it.qhalf;
+        n_a = uniform(it.n);
+        paired_a = uniform(it.paired);
+        qh_a = uniform(it.qhalf);
         nx = paired_a ? (n_a + 1) / 2 * 2 : 2 * n_a;
       }
       const int st = x & 1;
@@ -384,16 +444,13 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
           if (!warp_wait(bar(L::B_QF + half), (qf >> half) & 1, abort_flag)) return false;
           qf ^= 1 << half;
         }
-        if (!warp_wait(bar(L::B_KF + ks), kph, abort_flag)) return false;
+        // (a tile that both streams use was waited for by stream 0's step)
+        if ((paired_a || st == 0) && !warp_wait(bar(L::B_KF + ks), kph, abort_flag)) return false;
         tc_fence_after();
         const uint64_t qd = desc_sw128(sb + half * kTile, 16, 1024);
         const uint64_t kd = desc_sw128(sb + L::kRing + ks * kTile, 16, 1024);
         const uint32_t d = tbase + (uint32_t)st * 128;
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint32_t off = (k >> 2) * kSpan + (k & 3) * 32;
-          mma_ss_w(d, desc_adv(qd, off), desc_adv(kd, off), idS, k > 0);
-        }
+        mma_scores<D>(d, qd, kd, idS);
         mma_commit_w(bar(L::B_SF + st));
         if (paired_a || st == 1) {             // the last use of this K tile
           mma_commit_w(bar(L::B_KE + ks));
@@ -412,8 +469,9 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
     bool ok = score_step() && score_step();
     for (int b = 0; ok; ++b) {
       if (!item_wait(b)) break;
-      const int live = items[b % kItems].live, n_b = items[b % kItems].n, paired_b = items[b % kItems].paired;
-      if (!live) break;
+      const TileItem& itb = items[b % kItems];
+      if (!uniform(itb.live)) break;
+      const int n_b = uniform(itb.n), paired_b = uniform(itb.paired);
       const int real = paired_b ? n_b : 2 * n_b, ny = (real + 1) / 2 * 2;
       for (int y = 0; y < ny; ++y) {
         const int st = y & 1;
@@ -424,12 +482,11 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
           }
           if (!warp_wait(bar(L::B_PR + st), (pr >> st) & 1, abort_flag)) { ok = false; break; }
           pr ^= 1 << st;
-          if (!warp_wait(bar(L::B_KF + vs), vph, abort_flag)) { ok = false; break; }
+          if ((paired_b || st == 0) && !warp_wait(bar(L::B_KF + vs), vph, abort_flag)) { ok = false; break; }
           tc_fence_after();
           const uint64_t vd = desc_sw128(sb + L::kRing + vs * kTile, kSpan, 1024);
           const uint32_t pa = tbase + (uint32_t)st * 128, od = tbase + kColO + (uint32_t)st * 128;
-#pragma unroll
-          for (int k = 0; k < 8; ++k) mma_ts_w(od, pa + k * 8, desc_adv(vd, k * 16 * 128), idO, (y >= 2 || k > 0));
+          mma_values(od, pa, vd, idO, y >= 2);
           if (paired_b || st == 1) {           // the last use of this V tile
             mma_commit_w(bar(L::B_KE + vs));
             vs += 2;
@@ -454,6 +511,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
     const int st = warp >> 2, wq = warp & 3, wr = wq * 32 + lane;
     const uint32_t lrow = tbase + ((uint32_t)(wq * 32) << 16);
     const uint32_t s_col = (uint32_t)st * 128, o_col = kColO + (uint32_t)st * 128;
+    const bool wide = (reinterpret_cast<uintptr_t>(O) & 31) == 0;
     float* ex = reinterpret_cast<float*>(smem + L::kExOff);   // [2][128]: stream 1's maxima, sums
     int sf = 0, od = 0, exp_ = 0;              // parities of the next completions
     bool ok = true;
@@ -462,9 +520,10 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
       const TileItem it = items[n % kItems];
       item_done(n);
       if (!it.live) break;
-      const int rbase = it.paired ? 0 : st * 128, r = rbase + wr;
-      const bool live_warp = rbase + wq * 32 < it.rv;
-      const int last = it.p0 + (it.r0 + min(r, it.rv - 1)) / p.group;   // the row's last visible key
+      const int rbase = it.paired ? 0 : st * p.half, r = rbase + wr;
+      const int rows = min(p.half, it.rv - rbase);                      // of this stream's tile
+      const bool mine = wr < rows, live_warp = wq * 32 < rows;
+      const int last = it.p0 + (it.r0 + (mine ? r : it.rv - 1)) / p.group;   // the row's last visible key
       const int p_first = it.p0 + it.r0 / p.group;
       const int U = it.paired ? (it.n - st + 1) / 2 : it.n;             // this stream's steps
       float m_used = -INFINITY, l = 0.f;
@@ -601,11 +660,10 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
         m_used = M;
       }
       if (m_used == -INFINITY) l = 0.f;
-      const bool whole = it.slot < 0, mine = r < it.rv;
+      const bool whole = it.slot < 0;
       const float inv = !whole ? 1.f : (l > 0.f ? 1.0f / l : (l == 0.f ? 0.f : l));
       const int rr = it.r0 + r;
       __nv_bfloat16* orow = O + ((int64_t)(it.row0 + rr / p.group) * p.Hq + it.h * p.group + rr % p.group) * D;
-      const size_t at = (size_t)(whole ? 0 : it.slot) * ws.rows_cap + r;
       if (live_warp) {
 #pragma unroll
         for (int k = 0; k < D / 32; ++k) {
@@ -622,19 +680,17 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
           }
           if (!mine) continue;
           if (whole) {
+            uint32_t u[16];
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-              reinterpret_cast<uint4*>(orow)[4 * k + q] =
-                  make_uint4(pack_bf16(z[8 * q], z[8 * q + 1]), pack_bf16(z[8 * q + 2], z[8 * q + 3]),
-                             pack_bf16(z[8 * q + 4], z[8 * q + 5]), pack_bf16(z[8 * q + 6], z[8 * q + 7]));
+            for (int q = 0; q < 16; ++q) u[q] = pack_bf16(z[2 * q], z[2 * q + 1]);
+            store64(orow + 32 * k, u, wide);
           } else {
 #pragma unroll
             for (int q = 0; q < 8; ++q)
-              reinterpret_cast<float4*>(ws.o + at * D)[8 * k + q] =
-                  make_float4(z[4 * q], z[4 * q + 1], z[4 * q + 2], z[4 * q + 3]);
+              ws.chunk<D>(it.slot, 8 * k + q)[r] = make_float4(z[4 * q], z[4 * q + 1], z[4 * q + 2], z[4 * q + 3]);
           }
         }
-        if (mine && !whole) *reinterpret_cast<float2*>(ws.ml + 2 * at) = make_float2(m_used, l);
+        if (mine && !whole) ws.state(it.slot)[r] = make_float2(m_used, l);
       }
       tc_fence_before();
       __syncwarp();
@@ -642,10 +698,11 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
         if (merge) mbar_arrive(bar(L::B_OF + 1));
         mbar_arrive(bar(L::B_OF + st));
       }
-      __threadfence_block();
       if (*unbounded_flag && mine) {
-        if (whole) add_unbounded(p, it.s, it.h, it.t0, it.n, p_first, it.hi, Vc, D, last, orow);
-        else add_unbounded(p, it.s, it.h, it.t0, it.n, p_first, it.hi, Vc, D, last, ws.o + at * D);
+        if (whole) add_unbounded(p, it.s, it.h, it.t0, it.n, p_first, it.hi, Vc, D, last, orow, 4);
+        else
+          add_unbounded(p, it.s, it.h, it.t0, it.n, p_first, it.hi, Vc, D, last,
+                        reinterpret_cast<float*>(ws.chunk<D>(it.slot, 0) + r), 4 * ws.rows_cap);
       }
     }
   }
@@ -659,15 +716,14 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
 }
 
 template <int D>
-sa_status launch(const CUtensorMap& mk, const CUtensorMap& mv, const void* Q, int64_t q_stride, const void* Vc,
-                 const Params& p, float scale, void* O, const Workspace& ws, cudaStream_t stream) {
+sa_status launch(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const void* Vc, const Params& p,
+                 float scale, void* O, const Workspace& ws, cudaStream_t stream) {
   auto kern = paged_attn_tc_kernel<D>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Lay<D>::smem_bytes) != cudaSuccess)
     return launch_status("cudaFuncSetAttribute(paged_attn_tc_kernel)");
   const cudaError_t le =
-      launch_pdl(kern, dim3(ws.ctas), dim3(kThreads), Lay<D>::smem_bytes, stream, mk, mv,
-                 static_cast<const __nv_bfloat16*>(Q), q_stride, static_cast<const __nv_bfloat16*>(Vc), p,
-                 scale * kLog2e, static_cast<__nv_bfloat16*>(O), ws);
+      launch_pdl(kern, dim3(ws.ctas), dim3(kThreads), Lay<D>::smem_bytes, stream, mq, mk, mv,
+                 static_cast<const __nv_bfloat16*>(Vc), p, scale * kLog2e, static_cast<__nv_bfloat16*>(O), ws);
   if (le != cudaSuccess) return fail(SA_ERR_CUDA, std::string("paged_attn_tc_kernel: ") + cudaGetErrorString(le));
   return launch_status("paged_attn_tc_kernel");
 }
@@ -677,18 +733,21 @@ sa_status launch(const CUtensorMap& mk, const CUtensorMap& mv, const void* Q, in
 sa_status paged_attn_tc(const void* Q, int64_t q_stride, const void* Kc, const void* Vc, const sa_paged_shape& s,
                         const paged::Params& p, float scale, void* O, const paged::Workspace& ws,
                         cudaStream_t stream) {
-  CUtensorMap mk, mv;
+  CUtensorMap mq, mk, mv;
   uint64_t outer = (uint64_t)s.P * s.Hkv;
   if (p.max_pages == 0) {
     // no pages: every length reads as 0 and nothing is loaded through the maps
     Kc = Vc = ws.o;
     outer = 1;
   }
-  if (!make_tmap_bf16_3d(&mk, Kc, s.d, s.page, outer, 64, s.page) ||
-      !make_tmap_bf16_3d(&mv, Vc, s.d, s.page, outer, 64, s.page))
-    return fail(SA_ERR_CUDA, "sa_paged_attn_fwd: cuTensorMapEncodeTiled failed for the caches");
-  return s.d == 128 ? launch<128>(mk, mv, Q, q_stride, Vc, p, scale, O, ws, stream)
-                    : launch<64>(mk, mv, Q, q_stride, Vc, p, scale, O, ws, stream);
+  if (s.T == 1) q_stride = (int64_t)s.Hq * s.d;   // a single row has no stride
+  const uint64_t page_elems = (uint64_t)s.d * s.page;
+  if (!make_tmap_bf16_3d(&mq, Q, s.d, s.Hq, s.T, s.d, q_stride, 64, p.group, p.half / p.group) ||
+      !make_tmap_bf16_3d(&mk, Kc, s.d, s.page, outer, s.d, page_elems, 64, s.page, 1) ||
+      !make_tmap_bf16_3d(&mv, Vc, s.d, s.page, outer, s.d, page_elems, 64, s.page, 1))
+    return fail(SA_ERR_CUDA, "sa_paged_attn_fwd: cuTensorMapEncodeTiled failed for Q and the caches");
+  return s.d == 128 ? launch<128>(mq, mk, mv, Vc, p, scale, O, ws, stream)
+                    : launch<64>(mq, mk, mv, Vc, p, scale, O, ws, stream);
 }
 
 uint32_t paged_tc_error_take() {

@@ -268,10 +268,12 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 
 }  // namespace tc
 
-// Host: builds a 3-D bf16 tensor map [outer][rows][cols] (cols innermost) with
-// a box of {box_cols, box_rows, 1} and 128-byte swizzle.  Returns false on
+// Host: builds a 3-D bf16 tensor map [outer][rows][cols] (cols innermost, the
+// strides of rows and of the outer axis in elements) with a box of
+// {box_cols, box_rows, box_outer} and 128-byte swizzle.  Returns false on
 // failure.
 bool make_tmap_bf16_3d(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows, uint64_t outer,
-                       uint32_t box_cols, uint32_t box_rows);
+                       uint64_t row_stride, uint64_t outer_stride, uint32_t box_cols, uint32_t box_rows,
+                       uint32_t box_outer);
 
 }  // namespace sa

@@ -429,7 +429,7 @@ sa_status sa_sfa_attn_fwd(const void* Qs, const void* Ks, const void* V, sa_dtyp
  * three calls can be captured into a graph and replayed with other lengths.
  *
  * S <= 4096 requests; page in {16, 32, 64, 128}; d in {64, 128}; Hq any
- * multiple of Hkv; max_pages * page <= 2^30; S * max_pages, P * Hkv and
+ * multiple of Hkv (up to 128 times in bf16); max_pages * page <= 2^30; S * max_pages, P * Hkv and
  * T * Hkv below 2^31, T * Hq <= 2^30 (else SA_ERR_UNSUPPORTED).  Lengths,
  * tables, slots and the free ring are read on the device and bounded there:
  * whatever they hold, nothing outside the given arrays is read or written. */

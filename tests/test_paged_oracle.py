@@ -139,6 +139,7 @@ def test_attention_refusals(lib):
     assert call(dict(S=5000)) == bd.SA_ERR_UNSUPPORTED
     assert call(dict(T=1 << 28)) == bd.SA_ERR_UNSUPPORTED             # T * Hq rows
     assert call(dtype=7) == bd.SA_ERR_UNSUPPORTED
+    assert call(dict(Hq=4 * 129), qs=1 << 20) == bd.SA_ERR_UNSUPPORTED   # query heads per KV head, bf16
     assert call(window=-1) == bd.SA_ERR_INVALID_ARG
     for scale in (0.0, -0.1, float("inf"), float("nan")):
         assert call(scale=scale) == bd.SA_ERR_INVALID_ARG, scale
