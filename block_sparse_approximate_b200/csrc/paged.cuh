@@ -26,6 +26,16 @@ namespace paged {
 
 constexpr int kMaxRequests = 4096;
 
+// Division of 0 <= n < 2^31 by a divisor that the host knows: a multiplication.
+struct FastDiv {
+  uint32_t d, mul, shift;
+  explicit FastDiv(uint32_t divisor) : d(divisor), mul(1), shift(0) {
+    while (((uint64_t)1 << shift) < d) ++shift;
+    mul = (uint32_t)(((((uint64_t)1 << shift) - d) << 32) / d + 1);
+  }
+  __device__ __forceinline__ int div(int n) const { return (int)((__umulhi((uint32_t)n, mul) + (uint32_t)n) >> shift); }
+};
+
 struct Params {
   const int32_t* q_start;   // [S+1]
   const int32_t* kv_len;    // [S]
@@ -33,10 +43,11 @@ struct Params {
   int S, T, Hq, Hkv, group, page_shift, P, max_pages;
   int window;               // 0: none; else below max_pages * page
   int bm, half;             // rows of an item; up to `half` rows are a half item
+  FastDiv by_group, by_heads, by_bm;   // of group, Hkv, bm
 };
 
-// Quotient of non-negative numbers; 32-bit division where both fit (a 64-bit
-// one costs a hundred instructions on the way to the first load).
+// Quotient of non-negative numbers; 32-bit division where both fit (the line is
+// cut before the first load, where a 64-bit one's hundred instructions show).
 __host__ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
   return ((a | b) >> 31) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
 }
@@ -101,7 +112,7 @@ __device__ __forceinline__ Item item_of(const Request& q, const Params& p, int j
   it.r0 = j * p.bm;
   it.rv = min(p.bm, q.n * p.group - it.r0);
   it.p0 = q.len - q.n;
-  const int p_lo = it.p0 + it.r0 / p.group, p_hi = it.p0 + (it.r0 + it.rv - 1) / p.group;
+  const int p_lo = it.p0 + p.by_group.div(it.r0), p_hi = it.p0 + p.by_group.div(it.r0 + it.rv - 1);
   it.lo = p.window > 0 ? max(0, p_lo - p.window + 1) : 0;
   it.hi = max(0, p_hi + 1);
   it.t0 = it.lo / TL::BN;
@@ -112,17 +123,17 @@ __device__ __forceinline__ Item item_of(const Request& q, const Params& p, int j
 template <class TL>
 __device__ __forceinline__ int item_cost(const Item& it) { return it.nt * it.unit + TL::kOver; }
 __device__ __forceinline__ int items_of(const Request& q, const Params& p) {
-  return (q.n * p.group + p.bm - 1) / p.bm;
+  return p.by_bm.div(q.n * p.group + p.bm - 1);
 }
 
-// Key tiles of an item that lie before the place x of its own stretch.
+// Key tiles of an item that lie before the place x >= 0 of its own stretch.
 __device__ __forceinline__ int tiles_before(int64_t x, int nt, int unit) {
-  return min(nt, (int)quotient(x, unit));
+  return x >= (int64_t)nt * unit ? nt : (int)((uint32_t)x / (uint32_t)unit);
 }
 
 template <class TL>
 __device__ __forceinline__ Shares cut_line(int64_t total, int ctas) {
-  const int64_t n = quotient(total, TL::kMinShare);
+  const int64_t n = total / TL::kMinShare;
   Shares s;
   s.parts = (int)(n < 1 ? 1 : (n < ctas ? n : ctas));
   s.each = quotient(total, s.parts);
@@ -183,6 +194,20 @@ __device__ int64_t lay_line(const Params& p, int64_t* pre, int64_t* tot) {
   return run;
 }
 
+// Who holds place w of the line: {request, its start, its end} (all threads;
+// out in shared memory, to be read behind a barrier).
+template <int kThreads>
+__device__ __forceinline__ void find_request(const Params& p, const int64_t* pre, int64_t w, int64_t* out) {
+  for (int s = threadIdx.x; s < p.S; s += kThreads) {
+    const int64_t a = s ? pre[s - 1] : 0, b = pre[s];
+    if (a <= w && w < b) {
+      out[0] = s;
+      out[1] = a;
+      out[2] = b;
+    }
+  }
+}
+
 // One warp walks the items of a share.
 template <class TL>
 struct Walker {
@@ -195,29 +220,26 @@ struct Walker {
     it = item_of<TL>(q, p, j);
     cost = item_cost<TL>(it);
   }
-  // The item that holds place w of the line, 0 <= w < its length.
-  __device__ void find(const Params& p, const int64_t* pre, int64_t w) {
+  // The item that holds place w of the line, 0 <= w < its length; `at`: the
+  // request that does (find_request).
+  __device__ void find(const Params& p, int at_request, int64_t first, int64_t end, int64_t w) {
     const int lane = threadIdx.x & 31;
-    int a = 0, b = p.S - 1;
-    while (a < b) {
-      const int m = (a + b) >> 1;
-      if (pre[m] > w) b = m;
-      else a = m + 1;
-    }
-    s = a;
-    const int64_t first = s ? pre[s - 1] : 0;
-    const int64_t head = quotient(pre[s] - first, p.Hkv);
-    h = (int)quotient(w - first, head);
-    int64_t at = first + h * head;
+    s = at_request;
     q = load_request(p, s);
+    const int64_t len = end - first;
+    const int64_t head = len >> 31 ? len / p.Hkv : (int64_t)p.by_heads.div((int)len);
+    h = p.Hkv == 1 ? 0 : (int)quotient(w - first, head);
+    int64_t at = first + h * head;
     nj = items_of(q, p);
     for (j = 0;; j += 32) {
       const int mine = j + lane < nj ? item_cost<TL>(item_of<TL>(q, p, j + lane)) : 0;
       int64_t end = mine;
+      if (nj > 1) {
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, end, o);
-        if (lane >= o) end += y;
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t y = __shfl_up_sync(0xffffffffu, end, o);
+          if (lane >= o) end += y;
+        }
       }
       const unsigned past = __ballot_sync(0xffffffffu, at + end > w);
       if (past) {

@@ -74,10 +74,12 @@ paged_attn_simt_kernel(const float* __restrict__ Q, int64_t q_stride, const floa
   if (tid == 0) ws.desc[c].valid = 0;
   if (total == 0 || c >= shares.parts) return;
   Walker<TL> w;
+  __shared__ int64_t found[3];
   const int64_t w0 = shares.start(c), w1 = shares.start(c + 1);
+  find_request<kSimtThreads>(p, pre, w0, found);
   bool more = true;
-  if (warp == 0) w.find(p, pre, w0);
   __syncthreads();                              // the line is read; its memory becomes the operands'
+  if (warp == 0) w.find(p, (int)found[0], found[1], found[2], w0);
   int emitted = 0;
   bool first = true;
 
@@ -117,7 +119,7 @@ paged_attn_simt_kernel(const float* __restrict__ Q, int64_t q_stride, const floa
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
       if (r < jb.rv) {
         const int rr = jb.r0 + r;
-        v = load4(Q + (int64_t)(jb.row0 + rr / p.group) * q_stride + (int64_t)(jb.h * p.group + rr % p.group) * D + e);
+        v = load4(Q + (int64_t)(jb.row0 + p.by_group.div(rr)) * q_stride + (int64_t)(jb.h * p.group + (rr - p.by_group.div(rr) * p.group)) * D + e);
         v.x *= scale2; v.y *= scale2; v.z *= scale2; v.w *= scale2;
       }
       *reinterpret_cast<float4*>(sq + r * DP + e) = v;
@@ -129,7 +131,7 @@ paged_attn_simt_kernel(const float* __restrict__ Q, int64_t q_stride, const floa
       m[i] = -INFINITY;
       l[i] = 0.f;
       const int r = ty + 16 * i;
-      last[i] = r < jb.rv ? jb.p0 + (jb.r0 + r) / p.group : -1;
+      last[i] = r < jb.rv ? jb.p0 + p.by_group.div(jb.r0 + r) : -1;
 #pragma unroll
       for (int k = 0; k < NC * 4; ++k) o[i][k] = 0.f;
     }
@@ -249,7 +251,7 @@ paged_attn_simt_kernel(const float* __restrict__ Q, int64_t q_stride, const floa
       const int rr = jb.r0 + r;
       if (jb.slot < 0) {
         const float inv = l[i] > 0.f ? 1.0f / l[i] : (l[i] == 0.f ? 0.f : l[i]);
-        float* dst = O + ((int64_t)(jb.row0 + rr / p.group) * p.Hq + jb.h * p.group + rr % p.group) * D + 4 * tx;
+        float* dst = O + ((int64_t)(jb.row0 + p.by_group.div(rr)) * p.Hq + jb.h * p.group + (rr - p.by_group.div(rr) * p.group)) * D + 4 * tx;
 #pragma unroll
         for (int n = 0; n < NC; ++n)
           *reinterpret_cast<float4*>(dst + 64 * n) =
@@ -367,7 +369,7 @@ paged_combine_kernel(Params p, Workspace ws, T* __restrict__ O) {
   if (!mine) return;
   const float inv = sum > 0.f ? 1.0f / sum : (sum == 0.f ? 0.f : sum);
   const int rr = d.r0 + r;
-  T* dst = O + ((int64_t)(d.row0 + rr / p.group) * p.Hq + d.h * p.group + rr % p.group) * D + 16 * blockIdx.y;
+  T* dst = O + ((int64_t)(d.row0 + p.by_group.div(rr)) * p.Hq + d.h * p.group + (rr - p.by_group.div(rr) * p.group)) * D + 16 * blockIdx.y;
 #pragma unroll
   for (int e = 0; e < 16; e += 8) store8(dst + e, acc + e, inv);
 }
@@ -468,7 +470,8 @@ extern "C" sa_status sa_paged_attn_fwd(const void* Q, int64_t q_row_stride, cons
   // tensor cores: 128-row tiles of whole tokens, two to an item
   const int half = tc ? 128 / group * group : 16, bm = tc ? 2 * half : kSimtRows;
   Params p{q_start, kv_len, table, shape.S, shape.T, shape.Hq, shape.Hkv, group, shift, shape.P,
-           keys ? shape.max_pages : 0, window >= most ? 0 : window, bm, half};
+           keys ? shape.max_pages : 0, window >= most ? 0 : window, bm, half, FastDiv(group), FastDiv(shape.Hkv),
+           FastDiv(bm)};
   Workspace ws;
   ws.desc = static_cast<Desc*>(workspace);
   ws.rows_cap = rows_cap(shape, tc ? 256 : kSimtRows);

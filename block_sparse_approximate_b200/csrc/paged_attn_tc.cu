@@ -227,8 +227,6 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                      const __grid_constant__ CUtensorMap tmV, const __nv_bfloat16* __restrict__ Vc, const Params p, float scale2, __nv_bfloat16* __restrict__ O, const Workspace ws) {
-  pdl_wait();
-  pdl_trigger();
   using L = Lay<D>;
   using TL = TcTiling;
   constexpr int NS = L::NS, NH = L::NH;
@@ -247,14 +245,8 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
   TileItem* items = reinterpret_cast<TileItem*>(smem + L::kItemOff);
   auto bar = [&](int k) { return sb + L::kBarOff + 8u * k; };
 
-  // the line, in the memory of the query tiles (loaded after the first item is handed out)
-  int64_t* pre = reinterpret_cast<int64_t*>(smem);
-  const int64_t total = lay_line<TL, kThreads>(p, pre, reinterpret_cast<int64_t*>(smem + L::kTotOff));
-  const Shares shares = cut_line<TL>(total, ws.ctas);
-  if (threadIdx.x == 0) ws.desc[c].valid = 0;
-  if (total == 0 || c >= shares.parts) return;
-
-  if (threadIdx.x == 0) {
+  // barriers and TMEM while the previous launch drains
+  if (threadIdx.x == 32) {
     for (int s = 0; s < 2; ++s) {
       mbar_init(bar(L::B_QF + s), 1);
       mbar_init(bar(L::B_QE + s), 1);
@@ -276,12 +268,29 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
     *abort_flag = 0;
     *unbounded_flag = 0;
     fence_barrier_init();
+    prefetch_tmap(&tmQ);
+    prefetch_tmap(&tmK);
+    prefetch_tmap(&tmV);
   }
   if (warp == 0) tmem_alloc(smem_u32(tmem_slot), 512);
+  pdl_wait();
+  pdl_trigger();
+  // the line, in the memory of the query tiles (loaded after the first item is handed out)
+  int64_t* pre = reinterpret_cast<int64_t*>(smem);
+  int64_t* found = reinterpret_cast<int64_t*>(smem + L::kTotOff) + kThreads / 32;
+  const int64_t total = lay_line<TL, kThreads>(p, pre, reinterpret_cast<int64_t*>(smem + L::kTotOff));
+  const Shares shares = cut_line<TL>(total, ws.ctas);
+  if (threadIdx.x == 0) ws.desc[c].valid = 0;
+  const bool idle = total == 0 || c >= shares.parts;
+  if (!idle) find_request<kThreads>(p, pre, shares.start(c), found);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = uniform(*tmem_slot);
+  if (idle) {
+    if (warp == 0) tmem_dealloc(tbase, 512);
+    return;
+  }
 
   // Item n of the ring: wait until it is handed out / give it back.
   auto item_wait = [&](int n) { return warp_wait(bar(L::B_IF + n % kItems), (n / kItems) & 1, abort_flag); };
@@ -295,7 +304,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
     regs_dec<kOtherRegs>();
     const int64_t w0 = shares.start(c), w1 = shares.start(c + 1);
     Walker<TL> w;
-    w.find(p, pre, w0);
+    w.find(p, (int)found[0], found[1], found[2], w0);
     int n = 0, qhalf = 1, kt = 0;
     for (bool more = true;;) {
       int ta = 0, tb = 0;
@@ -306,8 +315,8 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
         else if (w.it.nt == 0) {
           // no row of the item sees a key
           for (int x = lane; x < w.it.rv * (D / 8); x += 32) {
-            const int r = w.it.r0 + x / (D / 8);
-            *reinterpret_cast<uint4*>(O + ((int64_t)(w.q.row0 + r / p.group) * p.Hq + w.h * p.group + r % p.group) * D +
+            const int r = w.it.r0 + x / (D / 8), tok = p.by_group.div(r);
+            *reinterpret_cast<uint4*>(O + ((int64_t)(w.q.row0 + tok) * p.Hq + w.h * p.group + r - tok * p.group) * D +
                                       8 * (x % (D / 8))) = make_uint4(0, 0, 0, 0);
           }
           more = w.next(p);
@@ -336,10 +345,6 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
   } else if (warp == 8) {
     // ------------------------------------------------------------ producer
     regs_dec<kOtherRegs>();
-    if (lane == 0) {
-      prefetch_tmap(&tmK);
-      prefetch_tmap(&tmV);
-    }
     const int page = 1 << p.page_shift;
     const int boxes = (128 >> p.page_shift) * NH;    // of a whole tile
     const int pi = lane / NH, hf = lane % NH;
@@ -351,14 +356,20 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
       const TileItem it = items[n % kItems];
       item_done(n);
       if (!it.live) break;
+      // the pages of a tile are looked up one tile ahead (nothing looks at the
+      // loaded id before its tile's turn, so the load is not waited for)
+      const int32_t* row = p.table + (size_t)it.s * p.max_pages;
+      auto in_span = [&](int t) {
+        const int key = (it.t0 + t) * 128 + pi * page;
+        return t < it.n && lane < boxes && key < it.hi && key + page > it.lo;
+      };
+      int id_next = in_span(0) ? row[(it.t0 * 128 + pi * page) >> p.page_shift] : 0;
       for (int t = 0; ok && t < it.n; ++t) {
-        const int k0 = (it.t0 + t) * 128, key = k0 + pi * page;
-        const bool mine = lane < boxes && key < it.hi && key + page > it.lo;
-        int outer = p.P * p.Hkv;               // behind the pool: the box is filled with zeros
-        if (mine) {
-          const int id = p.table[(size_t)it.s * p.max_pages + (key >> p.page_shift)];
-          if (id >= 0 && id < p.P) outer = id * p.Hkv + it.h;
-        }
+        const bool mine = in_span(t);
+        const int id = id_next;
+        if (in_span(t + 1)) id_next = row[((it.t0 + t + 1) * 128 + pi * page) >> p.page_shift];
+        // behind the pool: the box is filled with zeros
+        const int outer = id >= 0 && id < p.P ? id * p.Hkv + it.h : p.P * p.Hkv;
         const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, mine)) * box_bytes;
         for (int kv = 0; kv < 2; ++kv) {
           const int s = seq % NS;
@@ -380,7 +391,6 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
   } else if (warp == 10) {
     // ------------------------------------------------------------ query loader
     regs_dec<kOtherRegs>();
-    if (lane == 0) prefetch_tmap(&tmQ);
     int loads = 0;                             // bit h: parity of the loads of query tile h
     bool ok = true;
     for (int n = 0; ok; ++n) {
@@ -388,7 +398,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
       const TileItem it = items[n % kItems];
       item_done(n);
       if (!it.live) break;
-      const int tok = it.row0 + it.r0 / p.group;
+      const int tok = it.row0 + p.by_group.div(it.r0);
       for (int hx = 0; hx < 2; ++hx) {
         if (it.paired && hx != it.qhalf) continue;
         if (!warp_wait(bar(L::B_QE + hx), ((loads >> hx) & 1) ^ 1, abort_flag)) {
@@ -403,7 +413,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
 #pragma unroll
           for (int hf = 0; hf < NH; ++hf)
             tma_load_3d(sb + hx * kTile + hf * kSpan, &tmQ, 64 * hf, it.h * p.group,
-                        tok + (it.paired ? 0 : hx * (p.half / p.group)), bar(L::B_QF + hx));
+                        tok + (it.paired ? 0 : hx * p.by_group.div(p.half)), bar(L::B_QF + hx));
         }
         __syncwarp();
       }
@@ -523,8 +533,8 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
       const int rbase = it.paired ? 0 : st * p.half, r = rbase + wr;
       const int rows = min(p.half, it.rv - rbase);                      // of this stream's tile
       const bool mine = wr < rows, live_warp = wq * 32 < rows;
-      const int last = it.p0 + (it.r0 + (mine ? r : it.rv - 1)) / p.group;   // the row's last visible key
-      const int p_first = it.p0 + it.r0 / p.group;
+      const int last = it.p0 + p.by_group.div(it.r0 + (mine ? r : it.rv - 1));   // the row's last visible key
+      const int p_first = it.p0 + p.by_group.div(it.r0);
       const int U = it.paired ? (it.n - st + 1) / 2 : it.n;             // this stream's steps
       float m_used = -INFINITY, l = 0.f;
       for (int u = 0; u < U; ++u) {
@@ -539,7 +549,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
           if (!warp_wait(bar(L::B_KF + s), (seq / NS) & 1, abort_flag)) { ok = false; break; }
           uint8_t* vrow = smem + L::kRing + s * kTile + wr * 128;
           const bool out = k0 + wr < it.lo || k0 + wr >= it.hi;
-#pragma unroll
+#pragma unroll 2
           for (int j = 0; j < 8 * NH; ++j) {
             uint4* q = reinterpret_cast<uint4*>(vrow + (j >> 3) * kSpan + (((j & 7) ^ (wr & 7)) << 4));
             if (out) {
@@ -611,7 +621,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
           tmem_st32(lrow + s_col, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
           tmem_st32(lrow + s_col + 32, *reinterpret_cast<uint32_t(*)[32]>(&v[32]));
           if (u >= 1 && __any_sync(0xffffffffu, need)) {
-#pragma unroll
+#pragma unroll 1
             for (int k = 0; k < D / 32; ++k) {
               uint32_t o[32];
               tmem_ld32(lrow + o_col + 32 * k, o);
@@ -663,10 +673,12 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
       const bool whole = it.slot < 0;
       const float inv = !whole ? 1.f : (l > 0.f ? 1.0f / l : (l == 0.f ? 0.f : l));
       const int rr = it.r0 + r;
-      __nv_bfloat16* orow = O + ((int64_t)(it.row0 + rr / p.group) * p.Hq + it.h * p.group + rr % p.group) * D;
+      const int tok = p.by_group.div(rr);
+      __nv_bfloat16* orow = O + ((int64_t)(it.row0 + tok) * p.Hq + it.h * p.group + rr - tok * p.group) * D;
       if (live_warp) {
-#pragma unroll
-        for (int k = 0; k < D / 32; ++k) {
+#pragma unroll 1
+        for (int k = 0; k < D / 32; ++k) {     // rolled, as the other loops off the tiles' path: code that
+                                               // is not there does not push the tiles' out of the caches (5%)
           uint32_t x[32], y[32];
           tmem_ld32(lrow + o_col + 32 * k, x);
           if (merge) tmem_ld32(lrow + kColO + 128 + 32 * k, y);
