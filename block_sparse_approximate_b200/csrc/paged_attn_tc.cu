@@ -51,8 +51,9 @@ constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
 constexpr uint32_t kSpan = 128 * 128;          // 128 rows x one 128-byte swizzle span
 constexpr uint32_t kColO = 256;
 constexpr float kLazy = 8.0f;                  // O is rescaled when the maximum grew by more than 2^8
-constexpr uint32_t kExpFma = 0x49u;            // exponential pairs (of eight) on the FMA pipe
+constexpr float kStaleSum = 65536.0f;          // a tile's exponentials sum to less, or its maximum is formed
 constexpr int kItems = 4;                      // item ring
+constexpr uint32_t kExpBits = 0x7f807f80u, kExpStep = 0x00800080u;   // exponents of two bf16
 
 struct TcTiling {
   static constexpr int BN = 128;
@@ -61,10 +62,24 @@ struct TcTiling {
   static constexpr int kUnit = 4, kUnitHalf = 3, kOver = 6, kMinShare = 3;
 };
 
+// An item as the walker hands it out.  The softmax warps read its fields here
+// when they need them instead of holding them in registers beside a row of S.
 struct TileItem {
   int live, s, h, row0, r0, rv, p0, lo, hi, t0, n, slot, paired, qhalf, kt, pad;
+  int rows[2], steps[2];                       // of each stream: rows, key tiles
+  // tiles t (of 0 .. n - 1) with t >= from or t < to: the stream's rows do not
+  // see them whole / some row of the item does not
+  struct { int mask_from, mask_to, screen_from, screen_to; } edge[2];
+  int pad2[4];
 };
-static_assert(sizeof(TileItem) == 64, "item ring layout");
+static_assert(sizeof(TileItem) == 128, "item ring layout");
+
+// Tiles t >= from hold a key behind position p_first, tiles t < to one left of
+// the window of position p_last (t counted from the tile at t0).
+__device__ __forceinline__ void edge_range(int p_first, int p_last, int window, int t0, int& from, int& to) {
+  from = p_first < 0 ? 0 : max(0, (p_first + 1) / 128 - t0);
+  to = window > 0 && p_last - window >= 0 ? max(0, (p_last - window) / 128 + 1 - t0) : 0;
+}
 
 template <int D>
 struct Lay {
@@ -78,7 +93,7 @@ struct Lay {
   static constexpr uint32_t kBarOff = kRing + NS * kTile;
   static constexpr uint32_t kSlotOff = (kBarOff + 8 * NBAR + 15) / 16 * 16;  // tmem base, abort, unbounded
   static constexpr uint32_t kItemOff = kSlotOff + 16;
-  static constexpr uint32_t kExOff = kItemOff + 64 * kItems;                 // stream 1's maxima and sums
+  static constexpr uint32_t kExOff = kItemOff + 128 * kItems;                 // stream 1's maxima and sums
   static constexpr uint32_t kTotOff = kExOff;                                // lay_line's totals, before the roles
   static constexpr uint32_t kEnd = kExOff + 2 * 128 * 4;
   static constexpr size_t smem_bytes = 1024 + kEnd;
@@ -173,8 +188,6 @@ __device__ __forceinline__ float fmax3_nan(float a, float b, float c) {
   asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
-
-__device__ __forceinline__ bool unbounded(uint32_t half) { return (half & 0x7f80u) == 0x7f80u; }
 
 // Whether some row of an item (first position p_first, keys below hi) does
 // not see the whole tile at k0.
@@ -330,8 +343,33 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
       const int paired = w.it.rv <= p.half;
       qhalf = paired ? 1 - qhalf : 1;          // half items alternate the two query tiles
       if (lane == 0) {
-        items[n % kItems] = TileItem{got, w.s, w.h, w.q.row0, w.it.r0, w.it.rv, w.it.p0, w.it.lo, w.it.hi,
-                                     w.it.t0 + ta, tb - ta, slot, paired, qhalf, kt, 0};
+        TileItem& to = items[n % kItems];
+        to.live = got;
+        to.s = w.s;
+        to.h = w.h;
+        to.row0 = w.q.row0;
+        to.r0 = w.it.r0;
+        to.rv = w.it.rv;
+        to.p0 = w.it.p0;
+        to.lo = w.it.lo;
+        to.hi = w.it.hi;
+        to.t0 = w.it.t0 + ta;
+        to.n = tb - ta;
+        to.slot = slot;
+        to.paired = paired;
+        to.qhalf = qhalf;
+        to.kt = kt;
+        const int p_first = w.it.p0 + p.by_group.div(w.it.r0);
+#pragma unroll
+        for (int st = 0; st < 2; ++st) {
+          const int first = paired ? 0 : st * p.half;
+          to.rows[st] = min(p.half, w.it.rv - first);
+          to.steps[st] = paired ? (tb - ta - st + 1) / 2 : tb - ta;
+          auto& e = to.edge[st];
+          edge_range(w.it.p0 + p.by_group.div(w.it.r0 + first), w.it.p0 + p.by_group.div(w.it.r0 + first + to.rows[st] - 1),
+                     p.window, to.t0, e.mask_from, e.mask_to);
+          edge_range(p_first, w.it.hi - 1, p.window, to.t0, e.screen_from, e.screen_to);
+        }
         if (got && !whole && ta == 0)
           ws.desc[c] = Desc{w.start, shares, 1, slot, w.it.unit, w.it.nt, w.q.row0, w.it.r0, w.it.rv, w.h};
         mbar_arrive(bar(L::B_IF + n % kItems));
@@ -524,49 +562,57 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
     const bool wide = (reinterpret_cast<uintptr_t>(O) & 31) == 0;
     float* ex = reinterpret_cast<float*>(smem + L::kExOff);   // [2][128]: stream 1's maxima, sums
     int sf = 0, od = 0, exp_ = 0;              // parities of the next completions
+    // the last key that this thread's row sees (of the item's last row for a thread without one)
+    auto row_last = [&](const TileItem& it) {
+      const int r = wr < it.rows[st] ? (it.paired ? 0 : st * p.half) + wr : it.rv - 1;
+      return it.p0 + p.by_group.div(it.r0 + r);
+    };
     bool ok = true;
     for (int n = 0; ok; ++n) {
       if (!item_wait(n)) break;
-      const TileItem it = items[n % kItems];
-      item_done(n);
-      if (!it.live) break;
-      const int rbase = it.paired ? 0 : st * p.half, r = rbase + wr;
-      const int rows = min(p.half, it.rv - rbase);                      // of this stream's tile
-      const bool mine = wr < rows, live_warp = wq * 32 < rows;
-      const int last = it.p0 + p.by_group.div(it.r0 + (mine ? r : it.rv - 1));   // the row's last visible key
-      const int p_first = it.p0 + p.by_group.div(it.r0);
-      const int U = it.paired ? (it.n - st + 1) / 2 : it.n;             // this stream's steps
+      const TileItem& it = items[n % kItems];
+      if (!it.live) {
+        item_done(n);
+        break;
+      }
+      const int U = it.steps[st];              // this stream's steps
+      const bool live_warp = wq * 32 < it.rows[st], mine = wr < it.rows[st];
       float m_used = -INFINITY, l = 0.f;
       for (int u = 0; u < U; ++u) {
-        const int t = it.paired ? 2 * u + st : u, k0 = (it.t0 + t) * 128;
+        const int t = it.paired ? 2 * u + st : u;
+        const bool screen = t >= it.edge[st].screen_from || t < it.edge[st].screen_to;
+        const bool mask = t >= it.edge[st].mask_from || t < it.edge[st].mask_to;
         // S is complete, and with it the product P V before it
         if (!warp_wait(bar(L::B_SF + st), sf, abort_flag)) { ok = false; break; }
         sf ^= 1;
-        const bool edge = edge_tile(p_first, it.hi, p.window, k0);
-        if (edge) {
+        if (screen) {
           // screen the V tile: thread wr takes row wr
-          const int seq = 2 * (it.kt + t) + 1, s = seq % NS;
+          const int seq = 2 * (it.kt + t) + 1, s = seq % NS, key = (it.t0 + t) * 128 + wr;
           if (!warp_wait(bar(L::B_KF + s), (seq / NS) & 1, abort_flag)) { ok = false; break; }
           uint8_t* vrow = smem + L::kRing + s * kTile + wr * 128;
-          const bool out = k0 + wr < it.lo || k0 + wr >= it.hi;
-#pragma unroll 2
-          for (int j = 0; j < 8 * NH; ++j) {
-            uint4* q = reinterpret_cast<uint4*>(vrow + (j >> 3) * kSpan + (((j & 7) ^ (wr & 7)) << 4));
-            if (out) {
-              *q = make_uint4(0, 0, 0, 0);
-            } else {
-              uint4 y = *q;
-              uint32_t* w = reinterpret_cast<uint32_t*>(&y);
-              bool hit = false;
+          auto chunk16 = [&](int j) {
+            return reinterpret_cast<uint4*>(vrow + (j >> 3) * kSpan + (((j & 7) ^ (wr & 7)) << 4));
+          };
+          if (key < it.lo || key >= it.hi) {
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                if (unbounded(w[e])) { w[e] &= 0xffff0000u; hit = true; }
-                if (unbounded(w[e] >> 16)) { w[e] &= 0xffffu; hit = true; }
-              }
-              if (hit) {
-                *unbounded_flag = 1;           // before the values go
-                __threadfence_block();
-                *q = y;
+            for (int j = 0; j < 8 * NH; ++j) *chunk16(j) = make_uint4(0, 0, 0, 0);
+          } else {
+            // an exponent of all ones carries into the half's top bit
+            uint32_t hit = 0;
+#pragma unroll
+            for (int j = 0; j < 8 * NH; ++j) {
+              const uint4 y = *chunk16(j);
+              hit |= ((y.x & kExpBits) + kExpStep) | ((y.y & kExpBits) + kExpStep) | ((y.z & kExpBits) + kExpStep) |
+                     ((y.w & kExpBits) + kExpStep);
+            }
+            if (hit & 0x80008000u) {
+              *unbounded_flag = 1;             // before the values go
+              __threadfence_block();
+#pragma unroll 1
+              for (int j = 0; j < 32 * NH; ++j) {
+                uint32_t* w = reinterpret_cast<uint32_t*>(chunk16(j >> 2)) + (j & 3);
+                const uint32_t top = ((*w & kExpBits) + kExpStep) & 0x80008000u;
+                *w &= ~((top >> 15) * 0xffffu);
               }
             }
           }
@@ -575,49 +621,76 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
         if (live_warp) {
           tc_fence_after();
           uint32_t v[128];
+          float sum, factor = 1.f;
+          bool need = false;
+          // v[e] = the pair e of exponentials as bf16, their sum in sm8
+          auto exps = [&](int from, int to, float ng, float (&sm8)[8]) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            tmem_ld32(lrow + s_col + 32 * k, *reinterpret_cast<uint32_t(*)[32]>(&v[32 * k]));
-          tmem_wait_ld();
-          if (edge) {
-            const int hi = last - k0, lo = p.window > 0 ? last - p.window + 1 - k0 : 0;
+            for (int e = from; e < to; ++e) {
+              float a0, a1;
+              ffma2(a0, a1, __uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]), scale2, scale2, ng, ng);
+              const float p0 = fast_exp2(a0), p1 = fast_exp2(a1);
+              fadd2(sm8[2 * (e & 3)], sm8[2 * (e & 3) + 1], p0, p1);
+              v[e] = pack_bf16(p0, p1);
+            }
+          };
+          auto add8 = [](const float (&x)[8]) {
+            return ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
+          };
+          // The maximum only keeps the exponentials in range, and a stale one
+          // does as long as the tile's exponentials sum to less than 2^16.  So
+          // the tile's own maximum is formed for a row's first keys, for masked
+          // tiles and when that check fails (as it does for NaN and inf), and
+          // otherwise the exponentials of a quarter of the row run while the
+          // next quarter comes from TMEM (6% of the kernel).  All of them run
+          // on MUFU: a share of 1/8 or 3/8 on the FMA pipe, as the block-sparse
+          // kernel has, cost 1 and 3%, since the MMA issuer shares that pipe's
+          // scheduler.
+          bool fresh = mask || __any_sync(0xffffffffu, mine && m_used == -INFINITY);
+          if (!fresh) {
+            float sm8[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            tmem_ld32(lrow + s_col, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
+            tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 128; ++e)
-              if (e > hi || e < lo) v[e] = __float_as_uint(-INFINITY);
+            for (int k = 0; k < 4; ++k) {
+              if (k < 3) tmem_ld32(lrow + s_col + 32 * (k + 1), *reinterpret_cast<uint32_t(*)[32]>(&v[32 * (k + 1)]));
+              exps(16 * k, 16 * k + 16, -m_used, sm8);
+              if (k < 3) tmem_wait_ld();
+            }
+            sum = add8(sm8);
+            fresh = !__all_sync(0xffffffffu, sum < kStaleSum || !mine);
           }
-          float mx8[8];
+          if (fresh) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) mx8[k] = -INFINITY;
+            for (int k = 0; k < 4; ++k)
+              tmem_ld32(lrow + s_col + 32 * k, *reinterpret_cast<uint32_t(*)[32]>(&v[32 * k]));
+            tmem_wait_ld();
+            if (mask) {
+              const int hi = row_last(it) - (it.t0 + t) * 128, lo = p.window > 0 ? hi - p.window + 1 : 0;
 #pragma unroll
-          for (int e = 0; e < 64; ++e)
-            mx8[e & 7] = fmax3_nan(mx8[e & 7], __uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
-          const float mx = fmax3_nan(fmax3_nan(mx8[0], mx8[1], mx8[2]), fmax3_nan(mx8[3], mx8[4], mx8[5]),
-                                     fmax3_nan(mx8[6], mx8[7], mx8[7]));
-          // a score that is NaN or +inf makes the row NaN (as inf - inf does)
-          const float m_tile = mx < INFINITY ? mx * scale2 : NAN;
-          const bool need = !(m_tile <= m_used + kLazy);
-          float factor = 1.f;
-          if (need) {
-            factor = fast_exp2(m_used - m_tile);
-            m_used = m_tile;
+              for (int e = 0; e < 128; ++e)
+                if (e > hi || e < lo) v[e] = __float_as_uint(-INFINITY);
+            }
+            float mx8[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) mx8[k] = -INFINITY;
+#pragma unroll
+            for (int e = 0; e < 64; ++e)
+              mx8[e & 7] = fmax3_nan(mx8[e & 7], __uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
+            const float mx = fmax3_nan(fmax3_nan(mx8[0], mx8[1], mx8[2]), fmax3_nan(mx8[3], mx8[4], mx8[5]),
+                                       fmax3_nan(mx8[6], mx8[7], mx8[7]));
+            // a score that is NaN or +inf makes the row NaN (as inf - inf does)
+            const float m_tile = mx < INFINITY ? mx * scale2 : NAN;
+            need = !(m_tile <= m_used + kLazy);
+            if (need) {
+              factor = fast_exp2(m_used - m_tile);
+              m_used = m_tile;
+            }
+            float sm8[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            exps(0, 64, m_used == -INFINITY ? 0.f : -m_used, sm8);   // no key seen yet: p = 2^-inf = 0
+            sum = add8(sm8);
           }
-          // a masked score gives p = 0 or, on the FMA pipe, 2^-126; a row that
-          // has seen no key keeps such sums until the first key scales them by
-          // 0, or to the end, where its maximum of -inf drops them
-          const float ng = m_used == -INFINITY ? 0.f : -m_used;
-          float sm8[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) sm8[k] = 0.f;
-#pragma unroll
-          for (int e = 0; e < 64; ++e) {
-            float a0, a1, p0, p1;
-            ffma2(a0, a1, __uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]), scale2, scale2, ng, ng);
-            if ((kExpFma >> (e & 7)) & 1u) exp2_poly2(a0, a1, p0, p1);
-            else { p0 = fast_exp2(a0); p1 = fast_exp2(a1); }
-            fadd2(sm8[2 * (e & 3)], sm8[2 * (e & 3) + 1], p0, p1);
-            v[e] = pack_bf16(p0, p1);
-          }
-          l = l * factor + (((sm8[0] + sm8[1]) + (sm8[2] + sm8[3])) + ((sm8[4] + sm8[5]) + (sm8[6] + sm8[7])));
+          l = l * factor + sum;
           tmem_st32(lrow + s_col, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
           tmem_st32(lrow + s_col + 32, *reinterpret_cast<uint32_t(*)[32]>(&v[32]));
           if (u >= 1 && __any_sync(0xffffffffu, need)) {
@@ -643,8 +716,8 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
         od ^= 1;
         tc_fence_after();
       }
-      const int U1 = it.n / 2;                 // stream 1's steps of a paired item
-      if (it.paired && st == 1) {
+      const bool paired = it.paired;
+      if (paired && st == 1) {
         // hand the state to stream 0 (which gives back O_1)
         if (U > 0) {
           ex[wr] = m_used;
@@ -653,10 +726,11 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(L::B_EX));
         }
+        item_done(n);
         continue;
       }
       float f0 = 1.f, f1 = 0.f;
-      const bool merge = it.paired && U1 > 0;
+      const bool merge = paired && it.steps[1] > 0;
       if (merge) {
         if (!warp_wait(bar(L::B_EX), exp_, abort_flag)) break;
         exp_ ^= 1;
@@ -669,8 +743,8 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
         l = l * f0 + l1 * f1;
         m_used = M;
       }
-      if (m_used == -INFINITY) l = 0.f;
-      const bool whole = it.slot < 0;
+      const int slot = it.slot, r = (paired ? 0 : st * p.half) + wr;
+      const bool whole = slot < 0;
       const float inv = !whole ? 1.f : (l > 0.f ? 1.0f / l : (l == 0.f ? 0.f : l));
       const int rr = it.r0 + r;
       const int tok = p.by_group.div(rr);
@@ -699,10 +773,10 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
           } else {
 #pragma unroll
             for (int q = 0; q < 8; ++q)
-              ws.chunk<D>(it.slot, 8 * k + q)[r] = make_float4(z[4 * q], z[4 * q + 1], z[4 * q + 2], z[4 * q + 3]);
+              ws.chunk<D>(slot, 8 * k + q)[r] = make_float4(z[4 * q], z[4 * q + 1], z[4 * q + 2], z[4 * q + 3]);
           }
         }
-        if (mine && !whole) ws.state(it.slot)[r] = make_float2(m_used, l);
+        if (mine && !whole) ws.state(slot)[r] = make_float2(m_used, l);
       }
       tc_fence_before();
       __syncwarp();
@@ -711,11 +785,13 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
         mbar_arrive(bar(L::B_OF + st));
       }
       if (*unbounded_flag && mine) {
+        const int p_first = it.p0 + p.by_group.div(it.r0), last = row_last(it);
         if (whole) add_unbounded(p, it.s, it.h, it.t0, it.n, p_first, it.hi, Vc, D, last, orow, 4);
         else
           add_unbounded(p, it.s, it.h, it.t0, it.n, p_first, it.hi, Vc, D, last,
-                        reinterpret_cast<float*>(ws.chunk<D>(it.slot, 0) + r), 4 * ws.rows_cap);
+                        reinterpret_cast<float*>(ws.chunk<D>(slot, 0) + r), 4 * ws.rows_cap);
       }
+      item_done(n);
     }
   }
   __syncwarp();
