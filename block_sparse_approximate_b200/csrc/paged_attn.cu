@@ -17,8 +17,11 @@ using namespace paged;
 // Tiles of 64 rows and 64 keys, 256 threads, two CTAs per SM.  Thread (ty,
 // tx) holds scores of rows ty + 16 i and keys tx + 16 j (4 x 4) and outputs of
 // the same rows (d / 16 columns); a row's maximum and sum are reduced over
-// its 16 tx lanes, in 32 bits as the products are.  Bound by the FMA pipe for
-// prompts; items of up to 16 rows (decode) form only the row group i = 0.
+// its 16 tx lanes, in 32 bits as the products are.  K and V of a tile come by
+// cp.async, both before the scores, and the scores' exponentials take K's
+// place, so that two CTAs fit an SM and one's loads run beside the other's
+// products.  Bound by the FMA pipe for prompts; items of up to 16 rows
+// (decoding) form only the row group i = 0.
 constexpr int kSimtThreads = 256;
 constexpr int kSimtRows = 64;
 struct SimtTiling {
@@ -28,7 +31,6 @@ struct SimtTiling {
 };
 constexpr int kPitchP = 68;
 
-__device__ __forceinline__ float4 load4(const float* p) { return __ldg(reinterpret_cast<const float4*>(p)); }
 __device__ __forceinline__ void store8(float* dst, const float* x, float f) {
   reinterpret_cast<float4*>(dst)[0] = make_float4(x[0] * f, x[1] * f, x[2] * f, x[3] * f);
   reinterpret_cast<float4*>(dst)[1] = make_float4(x[4] * f, x[5] * f, x[6] * f, x[7] * f);
@@ -45,7 +47,16 @@ __device__ __forceinline__ void store8(__nv_bfloat16* dst, const float* x, float
 }
 
 template <int D>
-constexpr size_t simt_smem() { return (size_t)(2 * 64 * (D + 4) + 64 * kPitchP) * 4; }
+constexpr size_t simt_smem() { return (size_t)(3 * 64 * (D + 4)) * 4; }
+static_assert(kPitchP <= 64 + 4, "the exponentials lie in K's tile");
+
+__device__ __forceinline__ void copy16_or_zero(float* dst, const float* src, bool copy) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+               ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src), "r"(copy ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 template <int D>
 __global__ void __launch_bounds__(kSimtThreads, 2)
@@ -57,8 +68,9 @@ paged_attn_simt_kernel(const float* __restrict__ Q, int64_t q_stride, const floa
   constexpr int DP = D + 4, NC = D / 64;        // NC float4 columns of the output per thread
   extern __shared__ __align__(16) float smem_f[];
   float* sq = smem_f;
-  float* skv = sq + 64 * DP;
-  float* sp = skv + 64 * DP;
+  float* sk = sq + 64 * DP;
+  float* sv = sk + 64 * DP;
+  float* sp = sk;                               // after the scores
   __shared__ int64_t tot[kSimtThreads / 32];
   struct Job {
     int live, s, h, row0, r0, rv, p0, lo, hi, t0, ta, tb, slot;   // slot < 0: the whole item
@@ -113,16 +125,42 @@ paged_attn_simt_kernel(const float* __restrict__ Q, int64_t q_stride, const floa
     const Job jb = job;
     if (!jb.live) return;
 
+    // K and V of the tile at k0; rows outside the item's span and pages outside the pool read as zero
+    constexpr int IT = D / 16, RI = kSimtThreads / (D / 4);   // chunks of a thread, RI rows apart
+    const int row0 = tid / (D / 4), e0 = 4 * (tid % (D / 4));
+    const int mask = (1 << p.page_shift) - 1;
+    auto issue_tile = [&](int k0) {
+      int64_t src[IT];
+#pragma unroll
+      for (int k = 0; k < IT; ++k) {
+        const int key = k0 + row0 + RI * k;
+        src[k] = -1;
+        if (key >= jb.lo && key < jb.hi) src[k] = p.table[(size_t)jb.s * p.max_pages + (key >> p.page_shift)];
+      }
+#pragma unroll
+      for (int k = 0; k < IT; ++k) {
+        const int key = k0 + row0 + RI * k;
+        src[k] = src[k] >= 0 && src[k] < p.P ? (((src[k] * p.Hkv + jb.h) << p.page_shift) + (key & mask)) * D + e0 : -1;
+        copy16_or_zero(sk + (row0 + RI * k) * DP + e0, Kc + max(src[k], (int64_t)0), src[k] >= 0);
+      }
+      copies_commit();
+#pragma unroll
+      for (int k = 0; k < IT; ++k)
+        copy16_or_zero(sv + (row0 + RI * k) * DP + e0, Vc + max(src[k], (int64_t)0), src[k] >= 0);
+      copies_commit();
+    };
+    if (jb.ta < jb.tb) issue_tile((jb.t0 + jb.ta) * 64);
     // queries, scaled to log2 units
-    for (int x = tid; x < 64 * (D / 4); x += kSimtThreads) {
-      const int r = x / (D / 4), e = 4 * (x % (D / 4));
+#pragma unroll
+    for (int k = 0; k < IT; ++k) {
+      const int r = row0 + RI * k;
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
       if (r < jb.rv) {
-        const int rr = jb.r0 + r;
-        v = load4(Q + (int64_t)(jb.row0 + p.by_group.div(rr)) * q_stride + (int64_t)(jb.h * p.group + (rr - p.by_group.div(rr) * p.group)) * D + e);
+        const int tok = p.by_group.div(jb.r0 + r), head = jb.h * p.group + jb.r0 + r - tok * p.group;
+        v = __ldg(reinterpret_cast<const float4*>(Q + (int64_t)(jb.row0 + tok) * q_stride + (int64_t)head * D + e0));
         v.x *= scale2; v.y *= scale2; v.z *= scale2; v.w *= scale2;
       }
-      *reinterpret_cast<float4*>(sq + r * DP + e) = v;
+      *reinterpret_cast<float4*>(sq + r * DP + e0) = v;
     }
     float m[4], l[4], o[4][NC * 4];
     int last[4];                                // the row's last visible key
@@ -131,23 +169,10 @@ paged_attn_simt_kernel(const float* __restrict__ Q, int64_t q_stride, const floa
       m[i] = -INFINITY;
       l[i] = 0.f;
       const int r = ty + 16 * i;
-      last[i] = r < jb.rv ? jb.p0 + p.by_group.div(jb.r0 + r) : -1;
+      last[i] = jb.p0 + p.by_group.div(jb.r0 + min(r, jb.rv - 1));
 #pragma unroll
       for (int k = 0; k < NC * 4; ++k) o[i][k] = 0.f;
     }
-    const int mask = (1 << p.page_shift) - 1;
-    auto load_tile = [&](const float* cache, int k0) {
-      for (int x = tid; x < 64 * (D / 4); x += kSimtThreads) {
-        const int r = x / (D / 4), e = 4 * (x % (D / 4)), key = k0 + r;
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (key >= jb.lo && key < jb.hi) {
-          const int id = p.table[(size_t)jb.s * p.max_pages + (key >> p.page_shift)];
-          if (id >= 0 && id < p.P)
-            v = load4(cache + ((((int64_t)id * p.Hkv + jb.h) << p.page_shift) + (key & mask)) * D + e);
-        }
-        *reinterpret_cast<float4*>(skv + r * DP + e) = v;
-      }
-    };
     // one key tile; NI: row groups of 16 that hold rows
     auto tile = [&](auto ni, int k0) {
       constexpr int NI = decltype(ni)::value;
@@ -162,14 +187,14 @@ paged_attn_simt_kernel(const float* __restrict__ Q, int64_t q_stride, const floa
 #pragma unroll
         for (int i = 0; i < NI; ++i) a[i] = *reinterpret_cast<const float4*>(sq + (ty + 16 * i) * DP + e);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const float4*>(skv + (tx + 16 * j) * DP + e);
+        for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const float4*>(sk + (tx + 16 * j) * DP + e);
 #pragma unroll
         for (int i = 0; i < NI; ++i)
 #pragma unroll
           for (int j = 0; j < 4; ++j)
             s[i][j] = fmaf(a[i].x, b[j].x, fmaf(a[i].y, b[j].y, fmaf(a[i].z, b[j].z, fmaf(a[i].w, b[j].w, s[i][j]))));
       }
-      bool edge = false;                        // some row does not see the whole tile
+      __syncthreads();                          // K is read; its place takes the exponentials
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
         float mx = -INFINITY;
@@ -177,7 +202,6 @@ paged_attn_simt_kernel(const float* __restrict__ Q, int64_t q_stride, const floa
         for (int j = 0; j < 4; ++j) {
           const int key = k0 + tx + 16 * j;
           const bool seen = key <= last[i] && (p.window == 0 || key > last[i] - p.window);
-          edge |= !seen;
           s[i][j] = seen ? s[i][j] : -INFINITY;
           mx = fmaxf(mx, s[i][j]);
         }
@@ -200,9 +224,16 @@ paged_attn_simt_kernel(const float* __restrict__ Q, int64_t q_stride, const floa
 #pragma unroll
         for (int k = 0; k < NC * 4; ++k) o[i][k] *= f;
       }
-      const bool guard = __syncthreads_or(edge);           // scores stored, K read
-      load_tile(Vc, k0);
-      __syncthreads();
+      copies_wait<0>();                         // V has come
+      // 0 times a value that is not finite is not 0: such a tile takes the
+      // products that leave the masked keys out
+      bool finite = true;
+#pragma unroll
+      for (int k = 0; k < IT; ++k) {
+        const float4 v = *reinterpret_cast<const float4*>(sv + (row0 + RI * k) * DP + e0);
+        finite &= fabsf(v.x) < INFINITY && fabsf(v.y) < INFINITY && fabsf(v.z) < INFINITY && fabsf(v.w) < INFINITY;
+      }
+      const bool guard = __syncthreads_or(!finite);
       auto product = [&](auto guarded) {
 #pragma unroll 4
         for (int k = 0; k < 64; k += 4) {
@@ -213,7 +244,7 @@ paged_attn_simt_kernel(const float* __restrict__ Q, int64_t q_stride, const floa
           for (int kk = 0; kk < 4; ++kk) {
             float4 b[NC];
 #pragma unroll
-            for (int n = 0; n < NC; ++n) b[n] = *reinterpret_cast<const float4*>(skv + (k + kk) * DP + 4 * tx + 64 * n);
+            for (int n = 0; n < NC; ++n) b[n] = *reinterpret_cast<const float4*>(sv + (k + kk) * DP + 4 * tx + 64 * n);
 #pragma unroll
             for (int i = 0; i < NI; ++i) {
               const float e = kk == 0 ? a[i].x : kk == 1 ? a[i].y : kk == 2 ? a[i].z : a[i].w;
@@ -238,11 +269,12 @@ paged_attn_simt_kernel(const float* __restrict__ Q, int64_t q_stride, const floa
     };
     for (int t = jb.ta; t < jb.tb; ++t) {
       const int k0 = (jb.t0 + t) * 64;
-      __syncthreads();                          // the previous tile's V is read
-      load_tile(Kc, k0);
+      copies_wait<1>();                         // K has come
       __syncthreads();
       if (jb.rv <= 16) tile(std::integral_constant<int, 1>{}, k0);
       else tile(std::integral_constant<int, 4>{}, k0);
+      __syncthreads();                          // V and the exponentials are read
+      if (t + 1 < jb.tb) issue_tile(k0 + 64);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -251,7 +283,7 @@ paged_attn_simt_kernel(const float* __restrict__ Q, int64_t q_stride, const floa
       const int rr = jb.r0 + r;
       if (jb.slot < 0) {
         const float inv = l[i] > 0.f ? 1.0f / l[i] : (l[i] == 0.f ? 0.f : l[i]);
-        float* dst = O + ((int64_t)(jb.row0 + p.by_group.div(rr)) * p.Hq + jb.h * p.group + (rr - p.by_group.div(rr) * p.group)) * D + 4 * tx;
+        float* dst = O + ((int64_t)(jb.row0 + p.by_group.div(rr)) * p.Hq + jb.h * p.group + rr - p.by_group.div(rr) * p.group) * D + 4 * tx;
 #pragma unroll
         for (int n = 0; n < NC; ++n)
           *reinterpret_cast<float4*>(dst + 64 * n) =
@@ -369,7 +401,7 @@ paged_combine_kernel(Params p, Workspace ws, T* __restrict__ O) {
   if (!mine) return;
   const float inv = sum > 0.f ? 1.0f / sum : (sum == 0.f ? 0.f : sum);
   const int rr = d.r0 + r;
-  T* dst = O + ((int64_t)(d.row0 + p.by_group.div(rr)) * p.Hq + d.h * p.group + (rr - p.by_group.div(rr) * p.group)) * D + 16 * blockIdx.y;
+  T* dst = O + ((int64_t)(d.row0 + p.by_group.div(rr)) * p.Hq + d.h * p.group + rr - p.by_group.div(rr) * p.group) * D + 16 * blockIdx.y;
 #pragma unroll
   for (int e = 0; e < 16; e += 8) store8(dst + e, acc + e, inv);
 }

@@ -61,7 +61,8 @@ paged_plan_kernel(const int32_t* __restrict__ ctx_len, const int32_t* __restrict
   int* q_end = smem_plan;         // [S] rows up to and including s, at most T
   int* ask_end = q_end + S;       // [S] pages asked for; exact where the request is served
   int* give_end = ask_end + S;    // [S] pages handed back
-  int* served = give_end + S;     // [S]
+  int* owned = give_end + S;      // [S] pages held on entry; -1 - that for a refused request
+  int* shift_s = owned + S;       // [S] position of a row within its request, less the row
   __shared__ Sum3 tot[32];
   __shared__ int taken_all;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nthr = blockDim.x;
@@ -130,7 +131,8 @@ paged_plan_kernel(const int32_t* __restrict__ ctx_len, const int32_t* __restrict
       q_end[s] = (int)min(rows_incl, (int64_t)T);
       ask_end[s] = (int)min(ask_incl, (int64_t)0x7fffffff);
       give_end[s] = (int)(og + x.give);
-      served[s] = ok;
+      owned[s] = ok ? old : -1 - old;
+      shift_s[s] = ok ? (int)(ctx + (nw > 0 ? nw : 0) - rows_incl) : 0;
       if (ok && asks) atomicMax(&taken_all, (int)ask_incl);
       if (rank == 0) {
         if (s == 0) q_start[0] = 0;
@@ -145,40 +147,54 @@ paged_plan_kernel(const int32_t* __restrict__ ctx_len, const int32_t* __restrict
   const int rows = S ? q_end[S - 1] : 0;
   const int taken = taken_all, given = (int)run.give;
   const int first = rank * nthr + tid, step = nctas * nthr;
-  auto ring_at = [&](int64_t k) { return (int)((head + k) % P); };
-  // slots of the new tokens; a page below `old` stands in the table already,
-  // the others are still to come from the ring
-  for (int t = first; t < T; t += step) {
-    int64_t slot = -1;
-    if (t < rows) {
-      const int s = first_above(q_end, S, t);
-      if (served[s]) {
-        const int old = min(max(held[s], 0), max_pages);
-        const int pos = ctx_len[s] + t - (s ? q_end[s - 1] : 0);
-        const int cell = pos >> page_shift;
-        const int id = cell < old ? table[(size_t)s * max_pages + cell]
-                                  : ring[ring_at((int64_t)(s ? ask_end[s - 1] : 0) + cell - old)];
-        if (id >= 0 && id < P) slot = ((int64_t)id << page_shift) + (pos & (page - 1));
-      }
+  // (k stays below 2 P unless the state contradicts itself)
+  auto ring_at = [&](int64_t k) {
+    const int64_t x = head + k;
+    return (int)(x < P ? x : x < 2 * (int64_t)P ? x - P : x % P);
+  };
+  // slots of the new tokens; a page below `owned` stands in the table already,
+  // the others are still to come from the ring.  Four rows at a time, so that
+  // their searches and loads overlap (the search is a chain of shared-memory
+  // reads, the page id a load from L2).
+  for (int t0 = first; t0 < T; t0 += 4 * step) {
+    const int32_t* at[4];
+    int off[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int t = t0 + u * step;
+      at[u] = nullptr;
+      if (t >= rows) continue;
+      const int s = first_above(q_end, S, t), old = owned[s];
+      if (old < 0) continue;
+      const int pos = t + shift_s[s], cell = pos >> page_shift;
+      off[u] = pos & (page - 1);
+      at[u] = cell < old ? table + (size_t)s * max_pages + cell
+                         : ring + ring_at((int64_t)(s ? ask_end[s - 1] : 0) + cell - old);
     }
-    slots[t] = slot;
+    int id[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) id[u] = at[u] ? *at[u] : -1;
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (t0 + u * step < T)
+        slots[t0 + u * step] = id[u] >= 0 && id[u] < P ? ((int64_t)id[u] << page_shift) + off[u] : -1;
   }
   for (int k = first; k < taken; k += step) {
     const int s = first_above(ask_end, S, k);
-    const int cell = min(max(held[s], 0), max_pages) + k - (s ? ask_end[s - 1] : 0);
+    const int cell = owned[s] + k - (s ? ask_end[s - 1] : 0);
     table[(size_t)s * max_pages + cell] = ring[ring_at(k)];
   }
   for (int k = first; k < given; k += step) {
     const int s = first_above(give_end, S, k);
-    const int want = (int)(((int64_t)ctx_len[s] + new_len[s] + page - 1) >> page_shift);
-    int32_t* cell = table + (size_t)s * max_pages + want + k - (s ? give_end[s - 1] : 0);
+    // the last of the pages that s hands back is its last one
+    int32_t* cell = table + (size_t)s * max_pages + owned[s] - (give_end[s] - k);
     ring[ring_at((int64_t)count + k)] = *cell;
     *cell = -1;
   }
   cluster.sync();   // every CTA has read held and free_state
   if (rank == 0) {
     for (int s = tid; s < S; s += nthr)
-      if (served[s]) held[s] = (int)(((int64_t)ctx_len[s] + new_len[s] + page - 1) >> page_shift);
+      if (owned[s] >= 0) held[s] = (int)(((int64_t)ctx_len[s] + new_len[s] + page - 1) >> page_shift);
     if (tid == 0) {
       free_state[0] = ring_at(taken);
       free_state[1] = min(count - taken + given, P);
@@ -277,12 +293,15 @@ extern "C" sa_status sa_paged_plan(const int32_t* ctx_len, const int32_t* new_le
       return fail(SA_ERR_ALIGNMENT, "sa_paged_plan: 32-bit arrays must be 4-byte aligned");
   if (reinterpret_cast<uintptr_t>(slots) & 7u)
     return fail(SA_ERR_ALIGNMENT, "sa_paged_plan: slots must be 8-byte aligned");
-  // one CTA up to 1024 rows and requests; more of them from there, a power of two up to 8
+  // One CTA up to 1024 rows and requests, from there a cluster of a power of
+  // two up to 8; 512 threads each (8.4 us for 512 requests and 32615 rows,
+  // with 1024 threads, whose scan has twice the warps, 9.4; 4 CTAs 11.4) and
+  // 1024 where that saves a pass over the requests.
   const int work = std::max(shape.T, shape.S);
-  const int threads = work <= 256 ? 256 : 1024;
+  const int threads = work <= 256 ? 256 : shape.S <= 512 ? 512 : 1024;
   int ctas = 1;
   while (ctas < kPlanMaxCluster && ctas * 1024 < work) ctas *= 2;
-  const size_t smem = (size_t)shape.S * 4 * sizeof(int);
+  const size_t smem = (size_t)shape.S * 5 * sizeof(int);
   if (smem > 48 * 1024 &&
       cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return launch_status("cudaFuncSetAttribute(paged_plan_kernel)");
