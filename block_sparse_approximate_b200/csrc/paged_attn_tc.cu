@@ -52,6 +52,7 @@ constexpr uint32_t kSpan = 128 * 128;          // 128 rows x one 128-byte swizzl
 constexpr uint32_t kColO = 256;
 constexpr float kLazy = 8.0f;                  // O is rescaled when the maximum grew by more than 2^8
 constexpr float kStaleSum = 65536.0f;          // a tile's exponentials sum to less, or its maximum is formed
+constexpr int kFewTokens = 4;                  // a query tile of so few tokens is loaded token by token
 constexpr int kItems = 4;                      // item ring
 constexpr uint32_t kExpBits = 0x7f807f80u, kExpStep = 0x00800080u;   // exponents of two bf16
 
@@ -88,7 +89,7 @@ struct Lay {
   static constexpr int NS = D == 128 ? 5 : 10;
   static constexpr int B_QF = 0, B_QE = 2, B_KF = 4, B_KE = B_KF + NS, B_SF = B_KE + NS, B_PR = B_SF + 2,
                        B_OD = B_PR + 2, B_OF = B_OD + 2, B_EX = B_OF + 2, B_IF = B_EX + 1, B_IE = B_IF + kItems,
-                       B_FIN = B_IE + kItems, NBAR = B_FIN + 1;
+                       B_FIN = B_IE + kItems, B_QZ = B_FIN + 1, NBAR = B_QZ + 1;
   static constexpr uint32_t kRing = 2 * kTile;
   static constexpr uint32_t kBarOff = kRing + NS * kTile;
   static constexpr uint32_t kSlotOff = (kBarOff + 8 * NBAR + 15) / 16 * 16;  // tmem base, abort, unbounded
@@ -238,8 +239,9 @@ __device__ __forceinline__ void store64(void* dst, const uint32_t (&u)[16], bool
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                     const __grid_constant__ CUtensorMap tmV, const __nv_bfloat16* __restrict__ Vc, const Params p, float scale2, __nv_bfloat16* __restrict__ O, const Workspace ws) {
+paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmQ1,
+                     const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                     const __nv_bfloat16* __restrict__ Vc, const Params p, float scale2, __nv_bfloat16* __restrict__ O, const Workspace ws) {
   using L = Lay<D>;
   using TL = TcTiling;
   constexpr int NS = L::NS, NH = L::NH;
@@ -278,10 +280,12 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
     }
     mbar_init(bar(L::B_EX), 4);
     mbar_init(bar(L::B_FIN), 1);
+    mbar_init(bar(L::B_QZ), 8);
     *abort_flag = 0;
     *unbounded_flag = 0;
     fence_barrier_init();
     prefetch_tmap(&tmQ);
+    prefetch_tmap(&tmQ1);
     prefetch_tmap(&tmK);
     prefetch_tmap(&tmV);
   }
@@ -429,29 +433,57 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
   } else if (warp == 10) {
     // ------------------------------------------------------------ query loader
     regs_dec<kOtherRegs>();
+    // A tile of many tokens is one box per 64 channels (rows of other requests
+    // behind this one's may come along: a row of S depends on its own row of Q
+    // alone, and they are not stored).  A tile of few tokens (decoding) takes
+    // its tokens one by one and keeps the other rows zero: the MMAs multiply
+    // them all the same, and with zeros the tensor cores draw so much less
+    // power that a long run of decoding steps holds a higher clock (416 -> 388
+    // us for 128 sequences once the card is at its power limit).
     int loads = 0;                             // bit h: parity of the loads of query tile h
-    bool ok = true;
+    int dirty[2] = {0, 0};                     // rows of each tile that may not be zero
+    bool ok = warp_wait(bar(L::B_QZ), 0, abort_flag);
     for (int n = 0; ok; ++n) {
       if (!item_wait(n)) break;
-      const TileItem it = items[n % kItems];
-      item_done(n);
+      const TileItem& it = items[n % kItems];
       if (!it.live) break;
-      const int tok = it.row0 + p.by_group.div(it.r0);
+      const int first = it.row0 + p.by_group.div(it.r0), paired = it.paired, qhalf = it.qhalf, head = it.h * p.group;
+      const int rows0 = it.rows[0], rows1 = it.rows[1];
+      item_done(n);
+#pragma unroll
       for (int hx = 0; hx < 2; ++hx) {
-        if (it.paired && hx != it.qhalf) continue;
+        if (paired && hx != qhalf) continue;
         if (!warp_wait(bar(L::B_QE + hx), ((loads >> hx) & 1) ^ 1, abort_flag)) {
           ok = false;
           break;
         }
         loads ^= 1 << hx;
-        // rows of other requests behind this one's may come along: a row of S
-        // depends on its own row of Q alone, and they are not stored
-        if (lane == 0) {
-          mbar_expect_tx(bar(L::B_QF + hx), (uint32_t)(p.half * D * 2));
+        const int rows = paired || hx == 0 ? rows0 : rows1, tokens = p.by_group.div(rows);
+        const int tok = first + (paired ? 0 : hx * p.by_group.div(p.half));
+        if (tokens <= kFewTokens) {
+          for (int x = rows * 8 + lane; x < dirty[hx] * 8; x += 32)
 #pragma unroll
-          for (int hf = 0; hf < NH; ++hf)
-            tma_load_3d(sb + hx * kTile + hf * kSpan, &tmQ, 64 * hf, it.h * p.group,
-                        tok + (it.paired ? 0 : hx * p.by_group.div(p.half)), bar(L::B_QF + hx));
+            for (int hf = 0; hf < NH; ++hf)
+              *reinterpret_cast<uint4*>(smem + hx * kTile + hf * kSpan + 16 * x) = make_uint4(0, 0, 0, 0);
+          if (dirty[hx] > rows) fence_async();
+          dirty[hx] = rows;
+          __syncwarp();
+          if (lane == 0) {
+            mbar_expect_tx(bar(L::B_QF + hx), (uint32_t)(rows * D * 2));
+            for (int k = 0; k < tokens; ++k)
+#pragma unroll
+              for (int hf = 0; hf < NH; ++hf)
+                tma_load_3d(sb + hx * kTile + hf * kSpan + k * p.group * 128, &tmQ1, 64 * hf, head, tok + k,
+                            bar(L::B_QF + hx));
+          }
+        } else {
+          dirty[hx] = p.half;
+          if (lane == 0) {
+            mbar_expect_tx(bar(L::B_QF + hx), (uint32_t)(p.half * D * 2));
+#pragma unroll
+            for (int hf = 0; hf < NH; ++hf)
+              tma_load_3d(sb + hx * kTile + hf * kSpan, &tmQ, 64 * hf, head, tok, bar(L::B_QF + hx));
+          }
         }
         __syncwarp();
       }
@@ -557,6 +589,12 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
     // ------------------------------------------------------------ softmax
     regs_inc<kSoftmaxRegs>();
     const int st = warp >> 2, wq = warp & 3, wr = wq * 32 + lane;
+    // the query tiles start as zeros (the line that lay there is read)
+    for (int x = threadIdx.x - 128; x < (int)(2 * kTile / 16); x += 256)
+      reinterpret_cast<uint4*>(smem)[x] = make_uint4(0, 0, 0, 0);
+    fence_async();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(L::B_QZ));
     const uint32_t lrow = tbase + ((uint32_t)(wq * 32) << 16);
     const uint32_t s_col = (uint32_t)st * 128, o_col = kColO + (uint32_t)st * 128;
     const bool wide = (reinterpret_cast<uintptr_t>(O) & 31) == 0;
@@ -654,7 +692,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               if (k < 3) tmem_ld32(lrow + s_col + 32 * (k + 1), *reinterpret_cast<uint32_t(*)[32]>(&v[32 * (k + 1)]));
-              exps(16 * k, 16 * k + 16, -m_used, sm8);
+              exps(16 * k, 16 * k + 16, mine ? -m_used : -INFINITY, sm8);
               if (k < 3) tmem_wait_ld();
             }
             sum = add8(sm8);
@@ -687,7 +725,8 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
               m_used = m_tile;
             }
             float sm8[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-            exps(0, 64, m_used == -INFINITY ? 0.f : -m_used, sm8);   // no key seen yet: p = 2^-inf = 0
+            // no key seen yet: p = 2^-inf = 0; no row: p = 0 of its zeros
+            exps(0, 64, !mine ? -INFINITY : m_used == -INFINITY ? 0.f : -m_used, sm8);
             sum = add8(sm8);
           }
           l = l * factor + sum;
@@ -804,13 +843,13 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
 }
 
 template <int D>
-sa_status launch(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const void* Vc, const Params& p,
-                 float scale, void* O, const Workspace& ws, cudaStream_t stream) {
+sa_status launch(const CUtensorMap& mq, const CUtensorMap& mq1, const CUtensorMap& mk, const CUtensorMap& mv,
+                 const void* Vc, const Params& p, float scale, void* O, const Workspace& ws, cudaStream_t stream) {
   auto kern = paged_attn_tc_kernel<D>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Lay<D>::smem_bytes) != cudaSuccess)
     return launch_status("cudaFuncSetAttribute(paged_attn_tc_kernel)");
   const cudaError_t le =
-      launch_pdl(kern, dim3(ws.ctas), dim3(kThreads), Lay<D>::smem_bytes, stream, mq, mk, mv,
+      launch_pdl(kern, dim3(ws.ctas), dim3(kThreads), Lay<D>::smem_bytes, stream, mq, mq1, mk, mv,
                  static_cast<const __nv_bfloat16*>(Vc), p, scale * kLog2e, static_cast<__nv_bfloat16*>(O), ws);
   if (le != cudaSuccess) return fail(SA_ERR_CUDA, std::string("paged_attn_tc_kernel: ") + cudaGetErrorString(le));
   return launch_status("paged_attn_tc_kernel");
@@ -821,7 +860,7 @@ sa_status launch(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap
 sa_status paged_attn_tc(const void* Q, int64_t q_stride, const void* Kc, const void* Vc, const sa_paged_shape& s,
                         const paged::Params& p, float scale, void* O, const paged::Workspace& ws,
                         cudaStream_t stream) {
-  CUtensorMap mq, mk, mv;
+  CUtensorMap mq, mq1, mk, mv;
   uint64_t outer = (uint64_t)s.P * s.Hkv;
   if (p.max_pages == 0) {
     // no pages: every length reads as 0 and nothing is loaded through the maps
@@ -831,11 +870,12 @@ sa_status paged_attn_tc(const void* Q, int64_t q_stride, const void* Kc, const v
   if (s.T == 1) q_stride = (int64_t)s.Hq * s.d;   // a single row has no stride
   const uint64_t page_elems = (uint64_t)s.d * s.page;
   if (!make_tmap_bf16_3d(&mq, Q, s.d, s.Hq, s.T, s.d, q_stride, 64, p.group, p.half / p.group) ||
+      !make_tmap_bf16_3d(&mq1, Q, s.d, s.Hq, s.T, s.d, q_stride, 64, p.group, 1) ||
       !make_tmap_bf16_3d(&mk, Kc, s.d, s.page, outer, s.d, page_elems, 64, s.page, 1) ||
       !make_tmap_bf16_3d(&mv, Vc, s.d, s.page, outer, s.d, page_elems, 64, s.page, 1))
     return fail(SA_ERR_CUDA, "sa_paged_attn_fwd: cuTensorMapEncodeTiled failed for Q and the caches");
-  return s.d == 128 ? launch<128>(mq, mk, mv, Vc, p, scale, O, ws, stream)
-                    : launch<64>(mq, mk, mv, Vc, p, scale, O, ws, stream);
+  return s.d == 128 ? launch<128>(mq, mq1, mk, mv, Vc, p, scale, O, ws, stream)
+                    : launch<64>(mq, mq1, mk, mv, Vc, p, scale, O, ws, stream);
 }
 
 uint32_t paged_tc_error_take() {
