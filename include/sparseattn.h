@@ -506,6 +506,7 @@ size_t sa_paged_attn_workspace_size(sa_paged_shape shape);
  * whose row ranges overlap leave either one's output.  workspace:
  * at least sa_paged_attn_workspace_size() bytes, 256-byte aligned, contents
  * on entry do not matter; calls that may run at the same time need one each.
+ * O and the workspace overlap no other array.
  * The result does not depend on scheduling (no atomics).
  * Errors: SA_ERR_INVALID_ARG, SA_ERR_UNSUPPORTED, SA_ERR_ALIGNMENT,
  *         SA_ERR_WORKSPACE. */

@@ -205,6 +205,84 @@ def test_long_contexts_split_over_many_ctas(lib, dtype, Hq, Hkv):
     c.check(a)
 
 
+@pytest.mark.parametrize("dtype,d,Hq,Hkv,page,window", [(BF, 128, 12, 3, 16, 0), (BF, 64, 8, 4, 32, 50), (F32, 64, 4, 2, 64, 0)])
+def test_many_items_per_cta(lib, dtype, d, Hq, Hkv, page, window):
+    # far more items than CTAs, of one token, a few and many in turn (and of none): every CTA walks several of
+    # both kinds, splits the ones at its ends and reuses its query tiles, slots and accumulators
+    r = np.random.RandomState(12)
+    S = 260
+    ctx = r.randint(0, 400, S)
+    new = np.array([0, 1, 1, 2, 1, 5, 1, 1, 40, 1])[r.randint(0, 10, S)]
+    new[[3, 90, 200]] = (300, 170, 129)
+    c = Case(ctx, new, Hq, Hkv, d, page, dtype, seed=12, pad=2, window=window)
+    out = torch.full((c.T, Hq, d), 7.0, device=DEV, dtype=dtype)
+    c.run(out=out)
+    again = torch.full_like(out, 7.0)
+    c.run(out=again)
+    torch.cuda.synchronize()
+    assert_no_device_error()
+    assert torch.equal(out, again)
+    c.check(out)
+
+
+@pytest.mark.parametrize("group", [64, 100, 128])
+def test_many_query_heads_per_kv_head(lib, group):
+    c = Case([70, 300], [3, 1], group, 1, 128, 64, BF, seed=13)
+    out = c.run(out=torch.full((c.T, group, 128), 7.0, device=DEV, dtype=BF))
+    c.check(out)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_rising_scores(lib, dtype):
+    # each 128 keys score higher than the ones before, by 2^12 and then by 2^40: a maximum formed on
+    # earlier keys goes stale
+    c = Case([1300, 40], [2, 150], 4, 2, 128, 32, dtype, seed=14, poison=False)
+    c.Q = c.Q.clone()
+    c.Q[:] = 0
+    c.Q[..., 0] = 8.0
+    K = c.Kc.clone() * 0
+    for s in range(2):
+        for k in range(int(c.kv[s])):
+            step = (k // 128) * (12 if s else 40)
+            K[c.table[s, k // 32], :, k % 32, 0] = step / (8.0 * c.scale * math.log2(math.e)) + 0.1 * (k % 3)
+    c.Kc = K
+    out = c.run()
+    torch.cuda.synchronize()
+    O, A, seen = c.oracle()
+    err = np.abs(np64(out) - O)
+    w = (2.0 ** -8 + 2e-4 if dtype == BF else 2.0 ** -20) + 2 * 132 * 2.0 ** -24 * largest_score(c)
+    assert (err <= w * A + 2.0 ** -7 * np.abs(O) + 1e-6).all()
+
+
+def test_output_on_16_byte_boundary(lib):
+    c = Case([100, 7], [150, 1], 4, 2, 64, 16, BF, seed=15)
+    flat = torch.full((c.T * 4 * 64 + 8,), 7.0, device=DEV, dtype=BF)
+    out = flat[8:].view(c.T, 4, 64)
+    assert out.data_ptr() % 32 == 16
+    c.run(out=out)
+    c.check(out)
+    assert (flat[:8] == 7.0).all()
+
+
+def test_two_captured_graphs(lib):
+    # each graph's call takes its workspace from its own pool
+    cs = [Case([2000, 3], [100, 1], 8, 2, 128, 64, BF, seed=s, poison=False) for s in (16, 17)]
+    want = [c.run() for c in cs]
+    graphs, outs = [], []
+    for c in cs:
+        lists = c.lists
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(bd.paged_attn_fwd(c.Q, c.Kc, c.Vc, *lists, c.scale))
+        graphs.append(g)
+    for _ in range(3):
+        for g in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(want, outs):
+        assert torch.equal(a, b)
+
+
 def test_large_scores_and_shifts(lib):
     # scores of some hundreds in either direction, the largest one late: running maxima move by far
     c = Case([900, 300], [3, 150], 4, 2, 128, 32, BF, seed=7, poison=False)
