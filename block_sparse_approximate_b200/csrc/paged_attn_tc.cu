@@ -706,8 +706,15 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
             if (mask) {
               const int hi = row_last(it) - (it.t0 + t) * 128, lo = p.window > 0 ? hi - p.window + 1 : 0;
 #pragma unroll
-              for (int e = 0; e < 128; ++e)
-                if (e > hi || e < lo) v[e] = __float_as_uint(-INFINITY);
+              for (int k = 0; k < 4; ++k) {
+                // the columns 32 k + n that the row sees, bit n
+                const int h = hi - 32 * k, w = lo - 32 * k;
+                const uint32_t seen = (h >= 31 ? ~0u : h < 0 ? 0u : (2u << h) - 1u) & (w <= 0 ? ~0u : w > 31 ? 0u : ~0u << w);
+                if (__all_sync(0xffffffffu, seen == ~0u)) continue;
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  if (!((seen >> e) & 1u)) v[32 * k + e] = __float_as_uint(-INFINITY);
+              }
             }
             float mx8[8];
 #pragma unroll
