@@ -33,7 +33,9 @@ struct FastDiv {
     while (((uint64_t)1 << shift) < d) ++shift;
     mul = (uint32_t)(((((uint64_t)1 << shift) - d) << 32) / d + 1);
   }
-  __device__ __forceinline__ int div(int n) const { return (int)((__umulhi((uint32_t)n, mul) + (uint32_t)n) >> shift); }
+  __device__ __forceinline__ int div(int n) const {
+    return (int)((__umulhi((uint32_t)n, mul) + (uint32_t)n) >> shift);
+  }
 };
 
 struct Params {
@@ -44,6 +46,13 @@ struct Params {
   int window;               // 0: none; else below max_pages * page
   int bm, half;             // rows of an item; up to `half` rows are a half item
   FastDiv by_group, by_heads, by_bm;   // of group, Hkv, bm
+
+  // Row r of (the request whose rows start at row0, KV head h) as a row of the
+  // packed arrays: token * Hq + query head.
+  __device__ __forceinline__ int64_t query_row(int row0, int h, int r) const {
+    const int tok = by_group.div(r);
+    return (int64_t)(row0 + tok) * Hq + h * group + r - tok * group;
+  }
 };
 
 // Quotient of non-negative numbers; 32-bit division where both fit (the line is
@@ -291,6 +300,7 @@ struct Limits {
 
 // The bf16 attention on the tensor cores (paged_attn_tc.cu).
 sa_status paged_attn_tc(const void* Q, int64_t q_stride, const void* Kc, const void* Vc, const sa_paged_shape& s,
-                        const paged::Params& p, float scale, void* O, const paged::Workspace& ws, cudaStream_t stream);
+                        const paged::Params& p, float scale, void* O, const paged::Workspace& ws,
+                        cudaStream_t stream);
 
 }  // namespace sa

@@ -241,7 +241,8 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmQ1,
                      const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                     const __nv_bfloat16* __restrict__ Vc, const Params p, float scale2, __nv_bfloat16* __restrict__ O, const Workspace ws) {
+                     const __nv_bfloat16* __restrict__ Vc, const Params p, float scale2,
+                     __nv_bfloat16* __restrict__ O, const Workspace ws) {
   using L = Lay<D>;
   using TL = TcTiling;
   constexpr int NS = L::NS, NH = L::NH;
@@ -332,9 +333,8 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
         else if (w.it.nt == 0) {
           // no row of the item sees a key
           for (int x = lane; x < w.it.rv * (D / 8); x += 32) {
-            const int r = w.it.r0 + x / (D / 8), tok = p.by_group.div(r);
-            *reinterpret_cast<uint4*>(O + ((int64_t)(w.q.row0 + tok) * p.Hq + w.h * p.group + r - tok * p.group) * D +
-                                      8 * (x % (D / 8))) = make_uint4(0, 0, 0, 0);
+            __nv_bfloat16* row = O + p.query_row(w.q.row0, w.h, w.it.r0 + x / (D / 8)) * D;
+            *reinterpret_cast<uint4*>(row + 8 * (x % (D / 8))) = make_uint4(0, 0, 0, 0);
           }
           more = w.next(p);
         } else {
@@ -370,8 +370,9 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
           to.rows[st] = min(p.half, w.it.rv - first);
           to.steps[st] = paired ? (tb - ta - st + 1) / 2 : tb - ta;
           auto& e = to.edge[st];
-          edge_range(w.it.p0 + p.by_group.div(w.it.r0 + first), w.it.p0 + p.by_group.div(w.it.r0 + first + to.rows[st] - 1),
-                     p.window, to.t0, e.mask_from, e.mask_to);
+          const int r_first = w.it.r0 + first, r_last = r_first + to.rows[st] - 1;
+          edge_range(w.it.p0 + p.by_group.div(r_first), w.it.p0 + p.by_group.div(r_last), p.window, to.t0, e.mask_from,
+                     e.mask_to);
           edge_range(p_first, w.it.hi - 1, p.window, to.t0, e.screen_from, e.screen_to);
         }
         if (got && !whole && ta == 0)
@@ -709,7 +710,8 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
               for (int k = 0; k < 4; ++k) {
                 // the columns 32 k + n that the row sees, bit n
                 const int h = hi - 32 * k, w = lo - 32 * k;
-                const uint32_t seen = (h >= 31 ? ~0u : h < 0 ? 0u : (2u << h) - 1u) & (w <= 0 ? ~0u : w > 31 ? 0u : ~0u << w);
+                const uint32_t seen = (h >= 31 ? ~0u : h < 0 ? 0u : (2u << h) - 1u) &
+                                      (w <= 0 ? ~0u : w > 31 ? 0u : ~0u << w);
                 if (__all_sync(0xffffffffu, seen == ~0u)) continue;
 #pragma unroll
                 for (int e = 0; e < 32; ++e)
@@ -792,13 +794,12 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
       const int slot = it.slot, r = (paired ? 0 : st * p.half) + wr;
       const bool whole = slot < 0;
       const float inv = !whole ? 1.f : (l > 0.f ? 1.0f / l : (l == 0.f ? 0.f : l));
-      const int rr = it.r0 + r;
-      const int tok = p.by_group.div(rr);
-      __nv_bfloat16* orow = O + ((int64_t)(it.row0 + tok) * p.Hq + it.h * p.group + rr - tok * p.group) * D;
+      __nv_bfloat16* orow = O + p.query_row(it.row0, it.h, it.r0 + r) * D;
       if (live_warp) {
 #pragma unroll 1
-        for (int k = 0; k < D / 32; ++k) {     // rolled, as the other loops off the tiles' path: code that
-                                               // is not there does not push the tiles' out of the caches (5%)
+        for (int k = 0; k < D / 32; ++k) {
+          // rolled, as the other loops off the tiles' path: code that is not
+          // there does not push the tiles' out of the instruction caches (5%)
           uint32_t x[32], y[32];
           tmem_ld32(lrow + o_col + 32 * k, x);
           if (merge) tmem_ld32(lrow + kColO + 128 + 32 * k, y);

@@ -32,7 +32,8 @@ def _i32(a):
 class Case:
     """Pools with the requests' pages in random places; everything that no row may use is poisoned with NaN."""
 
-    def __init__(self, ctx, new, Hq, Hkv, d, page, dtype, seed, *, pad=0, spare=3, refuse=(), window=0, wide=0, poison=True):
+    def __init__(self, ctx, new, Hq, Hkv, d, page, dtype, seed, *, pad=0, spare=3, refuse=(), window=0, wide=0,
+                 poison=True):
         g = torch.Generator(device=DEV)
         g.manual_seed(seed)
         ctx, new = np.asarray(ctx), np.asarray(new)
@@ -205,7 +206,8 @@ def test_long_contexts_split_over_many_ctas(lib, dtype, Hq, Hkv):
     c.check(a)
 
 
-@pytest.mark.parametrize("dtype,d,Hq,Hkv,page,window", [(BF, 128, 12, 3, 16, 0), (BF, 64, 8, 4, 32, 50), (F32, 64, 4, 2, 64, 0)])
+@pytest.mark.parametrize("dtype,d,Hq,Hkv,page,window", [(BF, 128, 12, 3, 16, 0), (BF, 64, 8, 4, 32, 50),
+                                                        (F32, 64, 4, 2, 64, 0)])
 def test_many_items_per_cta(lib, dtype, d, Hq, Hkv, page, window):
     # far more items than CTAs, of one token, a few and many in turn (and of none): every CTA walks several of
     # both kinds, splits the ones at its ends and reuses its query tiles, slots and accumulators
@@ -403,7 +405,8 @@ def test_plan(lib, S, width, P, page, tokens):
 # --------------------------------------------------------------------------
 
 def _serve(lib, dtype, stream=None, graph=False):
-    """Three requests through prompts in chunks, decoding, an end and a newcomer; every row against whole-request attention."""
+    """Three requests through prompts in chunks, decoding, an end and a newcomer; every row against its whole
+    request's attention."""
     r = np.random.RandomState(11)
     Hq, Hkv, d, page = 6, 2, 64, 16
     eng = PagedServing(requests=3, max_pages=20, pages=31, page=page, tokens=96, Hq=Hq, Hkv=Hkv, d=d, dtype=dtype)
