@@ -489,14 +489,15 @@ def _paged_call(i: int, stream, fn: str, f, *args):
         _check(fn, status)
 
 
-def _paged_empty(shape, i: int, dtype, stream):
-    """torch.empty on the stream that will use it, so that the caching allocator's reuse stays ordered with it."""
-    if i < 0:
+def _paged_empty(like: torch.Tensor, shape, dtype, stream):
+    """An empty tensor on ``like``'s device and the stream that will use it, so that the caching allocator's
+    reuse stays ordered with it."""
+    if not like.is_cuda:
         raise ValueError("tensors must live on a CUDA device")
     if stream is None:
-        return torch.empty(shape, device=i, dtype=dtype)
+        return like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, device=i, dtype=dtype)
+        return like.new_empty(shape, dtype=dtype)
 
 
 def paged_plan(ctx_len: torch.Tensor, new_len: torch.Tensor, held: torch.Tensor, table: torch.Tensor,
@@ -512,11 +513,11 @@ def paged_plan(ctx_len: torch.Tensor, new_len: torch.Tensor, held: torch.Tensor,
         raise ValueError("new_len and held must be [S], table [S, max_pages], free_state [2]")
     i = ctx_len.get_device()
     if q_start is None:
-        q_start = _paged_empty((S + 1,), i, _I32, stream)
+        q_start = _paged_empty(ctx_len, S + 1, _I32, stream)
     if kv_len is None:
-        kv_len = _paged_empty((S,), i, _I32, stream)
+        kv_len = _paged_empty(ctx_len, S, _I32, stream)
     if slots is None:
-        slots = _paged_empty((tokens,), i, _I64, stream)
+        slots = _paged_empty(ctx_len, tokens, _I64, stream)
     if q_start.shape != (S + 1,) or kv_len.shape != (S,) or slots.shape != (tokens,):
         raise ValueError("q_start must be [S + 1], kv_len [S], slots [tokens]")
     ptr = _paged_ptr
@@ -562,14 +563,16 @@ def paged_attn_fwd(Q: torch.Tensor, Kcache: torch.Tensor, Vcache: torch.Tensor, 
         raise ValueError("the caches must be [P,Hkv,page,d] with Q's d")
     if rows != S or q_start.shape != (S + 1,):
         raise ValueError("q_start must be [S + 1], kv_len [S], table [S, max_pages]")
+    if not 0 <= window < 1 << 31:
+        raise ValueError("window must be 0 (none) or a number of keys below 2^31")
     i, dt, ptr, lib = Q.get_device(), Q.dtype, _paged_ptr, load()
     if out is None:
-        out = _paged_empty((T, Hq, d), i, dt, stream)
+        out = _paged_empty(Q, (T, Hq, d), dt, stream)
     elif out.shape != Q.shape:
         raise ValueError("out must have Q's shape")
     shape = PagedShape(S, T, Hq, Hkv, d, page, P, width)
     if workspace is None:
-        workspace = _paged_empty((max(lib.sa_paged_attn_workspace_size(shape), 256),), i, _U8, stream)
+        workspace = _paged_empty(Q, max(lib.sa_paged_attn_workspace_size(shape), 256), _U8, stream)
     _paged_call(i, stream, "sa_paged_attn_fwd", lib.sa_paged_attn_fwd, ptr(Q, i, dt, "Q", False), _paged_rows(Q, "Q"),
                 ptr(Kcache, i, dt, "Kcache"), ptr(Vcache, i, dt, "Vcache"), _dtype_code(Q), shape,
                 ptr(q_start, i, _I32, "q_start"), ptr(kv_len, i, _I32, "kv_len"), ptr(table, i, _I32, "table"),

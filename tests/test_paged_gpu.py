@@ -227,6 +227,29 @@ def test_many_items_per_cta(lib, dtype, d, Hq, Hkv, page, window):
     c.check(out)
 
 
+@pytest.mark.parametrize("S,dtype,d", [(1500, BF, 64), (4096, BF, 128), (1500, F32, 64)])
+def test_many_requests(lib, S, dtype, d):
+    # the line of requests is laid in several passes of the block
+    r = np.random.RandomState(18)
+    ctx, new = r.randint(0, 40, S), (r.rand(S) < 0.5).astype(int)
+    new[[0, S - 1, S // 2]] = (7, 3, 65)
+    c = Case(ctx, new, 4, 2, d, 16, dtype, seed=18, pad=1)
+    out = torch.full((c.T, 4, d), 7.0, device=DEV, dtype=dtype)
+    c.run(out=out)
+    torch.cuda.synchronize()
+    assert_no_device_error()
+    c.check(out)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_shared_pages(lib, dtype):
+    # requests that share the pages of a prefix, and one that lists a page twice
+    c = Case([200, 90, 64], [3, 40, 1], 4, 2, 128, 32, dtype, seed=19, poison=False)
+    c.table[1, :2] = c.table[0, :2]
+    c.table[2, 1] = c.table[2, 0]
+    c.check(c.run())
+
+
 @pytest.mark.parametrize("group", [64, 100, 128])
 def test_many_query_heads_per_kv_head(lib, group):
     c = Case([70, 300], [3, 1], group, 1, 128, 64, BF, seed=13)

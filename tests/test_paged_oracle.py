@@ -180,3 +180,6 @@ def test_binding_refuses_host_tensors_and_wrong_layouts():
     assert bd._paged_rows(torch.zeros(4, 9, 64)[:, 2:5], "x") == 9 * 64
     with pytest.raises(ValueError, match="q_start"):
         bd.paged_attn_fwd(x, c, c, i(2, 3), i(2), i(2), 1.0)
+    for window in (-1, 1 << 31, (1 << 32) + 5):
+        with pytest.raises(ValueError, match="window"):
+            bd.paged_attn_fwd(x, c, c, i(2, 3), i(3), i(2), 1.0, window=window)
