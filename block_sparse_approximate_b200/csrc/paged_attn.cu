@@ -379,7 +379,9 @@ paged_combine_kernel(Params p, Workspace ws, T* __restrict__ O) {
       for (int e = 0; e < 16; ++e) acc[e] *= f0;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        if (ml[j].x == -INFINITY) continue;     // no visible key in this portion, or no portion
+        // no visible key in this portion, or no portion; the sum tells, for the
+        // maximum of scores that are all NaN is -inf as well
+        if (ml[j].y == 0.f) continue;
         const float f = fast_exp2(ml[j].x - base);
         sum = fmaf(ml[j].y, f, sum);
 #pragma unroll
@@ -411,7 +413,7 @@ paged_combine_kernel(Params p, Workspace ws, T* __restrict__ O) {
     for (int e = 0; e < 16; ++e) acc[e] *= f0;
     for (int k = 1; k < step; ++k) {
       const float* x = red[tid + k * rows];
-      if (x[0] == -INFINITY) continue;
+      if (x[1] == 0.f) continue;
       const float f = fast_exp2(x[0] - base);
       sum = fmaf(x[1], f, sum);
 #pragma unroll

@@ -250,6 +250,27 @@ def test_shared_pages(lib, dtype):
     c.check(c.run())
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_queries_that_are_not_finite(lib, dtype, bad):
+    # a row's own Q reaches no other row, in chunks, single tokens and the padding alike
+    c = Case([300, 700, 0, 90, 0], [40, 1, 200, 3, 1], 8, 2, 128, 32, dtype, seed=20, pad=2)
+    hit = torch.zeros(c.T, c.Hq, dtype=torch.bool, device=DEV)
+    for t, h in [(0, 0), (17, 3), (39, 7), (40, 1), (41, 4), (100, 5), (242, 2), (244, 6)]:
+        hit[t, h] = True
+    hit[245:] = True
+    whole = c.Q.clone()
+    c.Q = whole.masked_fill(hit[..., None], bad)
+    out = c.run(out=torch.full((c.T, c.Hq, 128), 7.0, device=DEV, dtype=dtype))
+    assert_no_device_error()
+    c.Q = whole
+    rows = hit[:245]
+    assert out[:245][rows].isnan().all()
+    # (the rows hit are compared with nothing: they take the formula's value for the finite Q)
+    O = torch.from_numpy(c.oracle()[0]).to(DEV).to(dtype)
+    c.check(torch.where(hit[..., None] & (torch.arange(c.T, device=DEV) < 245)[:, None, None], O, out))
+
+
 @pytest.mark.parametrize("group", [64, 100, 128])
 def test_many_query_heads_per_kv_head(lib, group):
     c = Case([70, 300], [3, 1], group, 1, 128, 64, BF, seed=13)
