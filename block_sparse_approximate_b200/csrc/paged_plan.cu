@@ -191,7 +191,9 @@ paged_plan_kernel(const int32_t* __restrict__ ctx_len, const int32_t* __restrict
     ring[ring_at((int64_t)count + k)] = *cell;
     *cell = -1;
   }
-  cluster.sync();   // every CTA has read held and free_state
+  // every CTA has read held and free_state
+  if (nctas > 1) cluster.sync();
+  else __syncthreads();
   if (rank == 0) {
     for (int s = tid; s < S; s += nthr)
       if (owned[s] >= 0) held[s] = (int)(((int64_t)ctx_len[s] + new_len[s] + page - 1) >> page_shift);
@@ -318,7 +320,7 @@ extern "C" sa_status sa_paged_plan(const int32_t* ctx_len, const int32_t* new_le
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
+  cfg.numAttrs = ctas > 1 ? 2 : 1;   // a lone CTA needs no cluster
   const int shift = 31 - __builtin_clz((unsigned)shape.page);
   cudaLaunchKernelEx(&cfg, paged_plan_kernel, ctx_len, new_len, (int)shape.S, (int)shape.T, shift, (int)shape.P,
                      (int)shape.max_pages, held, table, free_pages, free_state, q_start, kv_len, slots);
