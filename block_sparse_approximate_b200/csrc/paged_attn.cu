@@ -150,19 +150,14 @@ paged_attn_simt_kernel(const float* __restrict__ Q, int64_t q_stride, const floa
         copy16_or_zero(sv + (row0 + RI * k) * DP + e0, Vc + max(src[k], (int64_t)0), src[k] >= 0);
       copies_commit();
     };
-    if (jb.ta < jb.tb) issue_tile((jb.t0 + jb.ta) * 64);
-    // queries, scaled to log2 units
+    // queries, in the group of the first K tile
 #pragma unroll
     for (int k = 0; k < IT; ++k) {
-      const int r = row0 + RI * k;
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (r < jb.rv) {
-        const int tok = p.by_group.div(jb.r0 + r), head = jb.h * p.group + jb.r0 + r - tok * p.group;
-        v = __ldg(reinterpret_cast<const float4*>(Q + (int64_t)(jb.row0 + tok) * q_stride + (int64_t)head * D + e0));
-        v.x *= scale2; v.y *= scale2; v.z *= scale2; v.w *= scale2;
-      }
-      *reinterpret_cast<float4*>(sq + r * DP + e0) = v;
+      const int r = row0 + RI * k, at = min(r, jb.rv - 1);
+      const int tok = p.by_group.div(jb.r0 + at), head = jb.h * p.group + jb.r0 + at - tok * p.group;
+      copy16_or_zero(sq + r * DP + e0, Q + (int64_t)(jb.row0 + tok) * q_stride + (int64_t)head * D + e0, r < jb.rv);
     }
+    if (jb.ta < jb.tb) issue_tile((jb.t0 + jb.ta) * 64);
     float m[4], l[4], o[4][NC * 4];
     int last[4];                                // the row's last visible key
 #pragma unroll
@@ -182,7 +177,7 @@ paged_attn_simt_kernel(const float* __restrict__ Q, int64_t q_stride, const floa
       for (int i = 0; i < NI; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
-#pragma unroll 8
+#pragma unroll 4
       for (int e = 0; e < D; e += 4) {
         float4 a[NI], b[4];
 #pragma unroll
@@ -196,35 +191,46 @@ paged_attn_simt_kernel(const float* __restrict__ Q, int64_t q_stride, const floa
             s[i][j] = fmaf(a[i].x, b[j].x, fmaf(a[i].y, b[j].y, fmaf(a[i].z, b[j].z, fmaf(a[i].w, b[j].w, s[i][j]))));
       }
       __syncthreads();                          // K is read; its place takes the exponentials
+      // (the rows' reductions side by side, so that their shuffles' latencies overlap)
+      float mx[NI], sum[NI];
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
-        float mx = -INFINITY;
+        mx[i] = -INFINITY;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int key = k0 + tx + 16 * j;
           const bool seen = key <= last[i] && (p.window == 0 || key > last[i] - p.window);
-          s[i][j] = seen ? s[i][j] : -INFINITY;
-          mx = fmaxf(mx, s[i][j]);
+          s[i][j] = seen ? s[i][j] * scale2 : -INFINITY;
+          mx[i] = fmaxf(mx[i], s[i][j]);
         }
+      }
 #pragma unroll
-        for (int d = 8; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-        const float mn = fmaxf(m[i], mx);
+      for (int d = 8; d > 0; d >>= 1)
+#pragma unroll
+        for (int i = 0; i < NI; ++i) mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], d));
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        const float mn = fmaxf(m[i], mx[i]);
         const float base = mn == -INFINITY ? 0.f : mn;     // no key yet: every term is 2^-inf = 0
         const float f = fast_exp2(m[i] - base);
         m[i] = mn;
-        float sum = 0.f;
+        sum[i] = 0.f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const float e = fast_exp2(s[i][j] - base);
-          sum += e;
+          sum[i] += e;
           sp[(ty + 16 * i) * kPitchP + tx + 16 * j] = e;
         }
-#pragma unroll
-        for (int d = 8; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-        l[i] = l[i] * f + sum;
+        l[i] *= f;
 #pragma unroll
         for (int k = 0; k < NC * 4; ++k) o[i][k] *= f;
       }
+#pragma unroll
+      for (int d = 8; d > 0; d >>= 1)
+#pragma unroll
+        for (int i = 0; i < NI; ++i) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], d);
+#pragma unroll
+      for (int i = 0; i < NI; ++i) l[i] += sum[i];
       copies_wait<0>();                         // V has come
       // 0 times a value that is not finite is not 0: such a tile takes the
       // products that leave the masked keys out
