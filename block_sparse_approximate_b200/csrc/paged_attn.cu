@@ -58,6 +58,170 @@ __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_
 template <int N>
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
+struct Job {
+  int live, s, h, row0, r0, rv, p0, lo, hi, t0, ta, tb, slot;   // slot < 0: the whole item
+};
+
+// Items of up to 8 rows (decoding).  The tiling above makes each warp read all
+// of K and V from shared memory for its two rows: 8192 cycles a tile for the
+// scores of two CTAs, shared memory's rate.  Here the D / 4 lanes that copy a
+// row of K or V are the ones that use it, each its own four channels, so the
+// groups of lanes run through their keys without a barrier, each with a
+// running maximum, sum and output of its own (joined once an item), and
+// memory is the bound (32 sequences, 8 / 2 heads of 128: 117 -> FEWUS us).
+//   scores: a lane's products of KB keys and R rows, KB R = the group's lanes,
+//   are summed over the group by halving: lanes exchange half of what they
+//   hold, and lane x ends with the sum of pair reversed(x) = key R + row.
+//   outputs: a lane's four columns of the R rows; the weights come by shuffle.
+constexpr int kFewRows = 8;
+
+template <int L>
+__host__ __device__ constexpr int reversed(int x) {
+  int y = 0;
+  for (int o = 1; o < L; o *= 2) y = 2 * y + ((x & o) != 0);
+  return y;
+}
+
+template <int D, int R, typename LookUp, typename Issue>
+__device__ __forceinline__ void few_rows(const Params& p, const Job& jb, float scale2, float* sq, float* sk, float* sv,
+                                         LookUp look_up, Issue issue, const float* Kc, const float* Vc, float* O,
+                                         const Workspace& ws) {
+  constexpr int DP = D + 4, L = D / 4, NG = kSimtThreads / L, IT = 64 / NG, KB = L / R, NB = IT / KB;
+  static_assert(KB * R == L && NB * KB == IT, "a batch of keys fills the group");
+  static_assert((size_t)NG * R * D <= 2 * 64 * DP && NG * R * 2 <= 64 * DP, "the groups' states fit the tiles");
+  const int tid = threadIdx.x, x = tid % L, grp = tid / L, e0 = 4 * x;
+  // this lane's pair: row and key of a batch
+  const int pair = (int)(__brev((unsigned)x) >> (L == 32 ? 27 : 28)), prow = pair % R, pkey = pair / R;
+  auto row_last = [&](int r) { return jb.p0 + p.by_group.div(jb.r0 + r); };
+  const int last = prow < jb.rv ? row_last(prow) : -1;
+  auto sees = [&](int row_end, int key) { return key <= row_end && (p.window == 0 || key > row_end - p.window); };
+  float q[R][4], o[R][4], m = -INFINITY, l = 0.f;
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) o[r][c] = 0.f;
+  copies_wait<1>();                             // K and the queries have come
+  __syncthreads();
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const float4 v = *reinterpret_cast<const float4*>(sq + r * DP + e0);
+    q[r][0] = v.x * scale2, q[r][1] = v.y * scale2, q[r][2] = v.z * scale2, q[r][3] = v.w * scale2;
+  }
+  for (int t = jb.ta; t < jb.tb; ++t) {
+    const int k0 = (jb.t0 + t) * 64;
+    const bool more = t + 1 < jb.tb;
+    if (t > jb.ta) copies_wait<1>();            // this lane's own part of K
+    if (more) look_up(k0 + 64);
+    float s[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      float v[L];
+#pragma unroll
+      for (int k = 0; k < KB; ++k) {
+        const float4 y = *reinterpret_cast<const float4*>(sk + (grp + NG * (b * KB + k)) * DP + e0);
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+          v[k * R + r] = fmaf(q[r][0], y.x, fmaf(q[r][1], y.y, fmaf(q[r][2], y.z, q[r][3] * y.w)));
+      }
+#pragma unroll
+      for (int o2 = 1, n = L / 2; o2 < L; o2 *= 2, n /= 2) {
+        const bool upper = x & o2;
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+          const float give = upper ? v[i] : v[i + n], keep = upper ? v[i + n] : v[i];
+          v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o2);
+        }
+      }
+      s[b] = sees(last, k0 + grp + NG * (b * KB + pkey)) ? v[0] : -INFINITY;
+    }
+    if (more) issue(k0 + 64, Kc, sk);
+    float mx = s[0];
+#pragma unroll
+    for (int b = 1; b < NB; ++b) mx = fmaxf(mx, s[b]);
+#pragma unroll
+    for (int o2 = 1; o2 < KB; o2 *= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o2));
+    const float mn = fmaxf(m, mx);
+    const float base = mn == -INFINITY ? 0.f : mn;     // no key yet: every term is 2^-inf = 0
+    const float f = fast_exp2(m - base);
+    m = mn;
+    l *= f;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      s[b] = fast_exp2(s[b] - base);
+      l += s[b];
+    }
+    if (__any_sync(0xffffffffu, f != 1.f))
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const float fr = __shfl_sync(0xffffffffu, f, reversed<L>(r), L);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) o[r][c] *= fr;
+      }
+    if (more) copies_wait<1>();                 // this lane's own part of V
+    else copies_wait<0>();
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int k = 0; k < KB; ++k) {
+        const int row = grp + NG * (b * KB + k);
+        const float4 y = *reinterpret_cast<const float4*>(sv + row * DP + e0);
+        float w[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) w[r] = __shfl_sync(0xffffffffu, s[b], reversed<L>(k * R + r), L);
+        // 0 times a value that is not finite is not 0: a key is left out for the rows that do not see it
+        const bool finite = fabsf(y.x) < INFINITY && fabsf(y.y) < INFINITY && fabsf(y.z) < INFINITY &&
+                            fabsf(y.w) < INFINITY;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          if (!finite && (r >= jb.rv || !sees(row_last(r), k0 + row))) continue;
+          o[r][0] = fmaf(w[r], y.x, o[r][0]);
+          o[r][1] = fmaf(w[r], y.y, o[r][1]);
+          o[r][2] = fmaf(w[r], y.z, o[r][2]);
+          o[r][3] = fmaf(w[r], y.w, o[r][3]);
+        }
+      }
+    __syncwarp();
+    if (more) issue(k0 + 64, Vc, sv);
+  }
+#pragma unroll
+  for (int o2 = 1; o2 < KB; o2 *= 2) l += __shfl_xor_sync(0xffffffffu, l, o2);
+  // the groups' states: outputs over K and V, maxima and sums over the queries
+  __syncthreads();
+  float2* ml = reinterpret_cast<float2*>(sq);
+  if (pkey == 0) ml[grp * R + prow] = make_float2(m, l);
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+    *reinterpret_cast<float4*>(sk + (grp * R + r) * D + e0) = make_float4(o[r][0], o[r][1], o[r][2], o[r][3]);
+  __syncthreads();
+  const int r = tid / L;                        // four columns of a row each
+  if (r >= jb.rv) return;
+  float M = -INFINITY, sum = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int g = 0; g < NG; ++g) M = fmaxf(M, ml[g * R + r].x);
+  const float base = M == -INFINITY ? 0.f : M;
+#pragma unroll
+  for (int g = 0; g < NG; ++g) {
+    const float2 y = ml[g * R + r];
+    if (y.y == 0.f) continue;                   // no key of the row with this group
+    const float f = fast_exp2(y.x - base);
+    const float4 v = *reinterpret_cast<const float4*>(sk + (g * R + r) * D + e0);
+    sum = fmaf(y.y, f, sum);
+    acc.x = fmaf(v.x, f, acc.x);
+    acc.y = fmaf(v.y, f, acc.y);
+    acc.z = fmaf(v.z, f, acc.z);
+    acc.w = fmaf(v.w, f, acc.w);
+  }
+  if (jb.slot < 0) {
+    const float inv = sum > 0.f ? 1.0f / sum : (sum == 0.f ? 0.f : sum);
+    *reinterpret_cast<float4*>(O + p.query_row(jb.row0, jb.h, jb.r0 + r) * D + e0) =
+        make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+  } else {
+    ws.chunk<D>(jb.slot, x)[r] = acc;
+    if (x == 0) ws.state(jb.slot)[r] = make_float2(M, sum);
+  }
+}
+
 template <int D>
 __global__ void __launch_bounds__(kSimtThreads, 2)
 paged_attn_simt_kernel(const float* __restrict__ Q, int64_t q_stride, const float* __restrict__ Kc,
@@ -72,9 +236,6 @@ paged_attn_simt_kernel(const float* __restrict__ Q, int64_t q_stride, const floa
   float* sv = sk + 64 * DP;
   float* sp = sk;                               // after the scores
   __shared__ int64_t tot[kSimtThreads / 32];
-  struct Job {
-    int live, s, h, row0, r0, rv, p0, lo, hi, t0, ta, tb, slot;   // slot < 0: the whole item
-  };
   __shared__ Job job;
   const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15, warp = tid >> 5, lane = tid & 31;
   const int c = blockIdx.x;
@@ -129,35 +290,48 @@ paged_attn_simt_kernel(const float* __restrict__ Q, int64_t q_stride, const floa
     constexpr int IT = D / 16, RI = kSimtThreads / (D / 4);   // chunks of a thread, RI rows apart
     const int row0 = tid / (D / 4), e0 = 4 * (tid % (D / 4));
     const int mask = (1 << p.page_shift) - 1;
-    auto issue_tile = [&](int k0) {
-      int64_t src[IT];
+    int id[IT];                                 // pages of this thread's rows of a tile, -1: none
+    auto look_up = [&](int k0) {
 #pragma unroll
       for (int k = 0; k < IT; ++k) {
         const int key = k0 + row0 + RI * k;
-        src[k] = -1;
-        if (key >= jb.lo && key < jb.hi) src[k] = p.table[(size_t)jb.s * p.max_pages + (key >> p.page_shift)];
+        id[k] = -1;
+        if (key >= jb.lo && key < jb.hi) id[k] = p.table[(size_t)jb.s * p.max_pages + (key >> p.page_shift)];
       }
+    };
+    auto issue = [&](int k0, const float* src, float* dst) {
 #pragma unroll
       for (int k = 0; k < IT; ++k) {
-        const int key = k0 + row0 + RI * k;
-        const bool there = src[k] >= 0 && src[k] < p.P;
-        src[k] = there ? (((src[k] * p.Hkv + jb.h) << p.page_shift) + (key & mask)) * D + e0 : -1;
-        copy16_or_zero(sk + (row0 + RI * k) * DP + e0, Kc + max(src[k], (int64_t)0), src[k] >= 0);
+        const bool there = id[k] >= 0 && id[k] < p.P;
+        const int64_t at = ((((int64_t)id[k] * p.Hkv + jb.h) << p.page_shift) + ((k0 + row0 + RI * k) & mask)) * D + e0;
+        copy16_or_zero(dst + (row0 + RI * k) * DP + e0, src + (there ? at : 0), there);
       }
-      copies_commit();
-#pragma unroll
-      for (int k = 0; k < IT; ++k)
-        copy16_or_zero(sv + (row0 + RI * k) * DP + e0, Vc + max(src[k], (int64_t)0), src[k] >= 0);
       copies_commit();
     };
-    // queries, in the group of the first K tile
+    auto issue_tile = [&](int k0) {
+      look_up(k0);
+      issue(k0, Kc, sk);
+      issue(k0, Vc, sv);
+    };
+    if (jb.ta < jb.tb) {
+      // queries, in the group of the first K tile
 #pragma unroll
-    for (int k = 0; k < IT; ++k) {
-      const int r = row0 + RI * k, at = min(r, jb.rv - 1);
-      const int tok = p.by_group.div(jb.r0 + at), head = jb.h * p.group + jb.r0 + at - tok * p.group;
-      copy16_or_zero(sq + r * DP + e0, Q + (int64_t)(jb.row0 + tok) * q_stride + (int64_t)head * D + e0, r < jb.rv);
+      for (int k = 0; k < IT; ++k) {
+        const int r = row0 + RI * k, at = min(r, jb.rv - 1);
+        const int tok = p.by_group.div(jb.r0 + at), head = jb.h * p.group + jb.r0 + at - tok * p.group;
+        copy16_or_zero(sq + r * DP + e0, Q + (int64_t)(jb.row0 + tok) * q_stride + (int64_t)head * D + e0, r < jb.rv);
+      }
+      issue_tile((jb.t0 + jb.ta) * 64);
     }
-    if (jb.ta < jb.tb) issue_tile((jb.t0 + jb.ta) * 64);
+    if (jb.rv <= kFewRows) {
+      auto few = [&](auto rows) {
+        few_rows<D, decltype(rows)::value>(p, jb, scale2, sq, sk, sv, look_up, issue, Kc, Vc, O, ws);
+      };
+      if (jb.rv <= 4) few(std::integral_constant<int, 4>{});
+      else few(std::integral_constant<int, 8>{});
+      __syncthreads();                          // job, queries and the groups' states are read
+      continue;
+    }
     float m[4], l[4], o[4][NC * 4];
     int last[4];                                // the row's last visible key
 #pragma unroll

@@ -250,6 +250,19 @@ def test_shared_pages(lib, dtype):
     c.check(c.run())
 
 
+@pytest.mark.parametrize("window", [0, 70])
+@pytest.mark.parametrize("d,page", [(64, 32), (128, 16)])
+@pytest.mark.parametrize("group", [1, 2, 4, 5, 8, 9, 16])
+def test_attention_few_rows_fp32(lib, group, d, page, window):
+    # items of one to some tens of rows: single tokens, a few of them, chunks whose last item has few rows
+    c = Case([0, 3, 63, 64, 130, 777, 40, 2500, 5], [1, 1, 1, 2, 3, 1, 66, 1, 4], 2 * group, 2, d, page, F32, seed=21,
+             pad=2, window=window)
+    out = torch.full((c.T, c.Hq, d), 7.0, device=DEV, dtype=F32)
+    c.run(out=out)
+    torch.cuda.synchronize()
+    c.check(out)
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
 def test_queries_that_are_not_finite(lib, dtype, bad):
