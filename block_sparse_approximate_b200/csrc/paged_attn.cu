@@ -68,11 +68,12 @@ struct Job {
 // row of K or V are the ones that use it, each its own four channels, so the
 // groups of lanes run through their keys without a barrier, each with a
 // running maximum, sum and output of its own (joined once an item), and
-// memory is the bound (32 sequences, 8 / 2 heads of 128: 117 -> FEWUS us).
+// memory is the bound (32 sequences, 8 / 2 heads of 128: 117 -> 48 us).
 //   scores: a lane's products of KB keys and R rows, KB R = the group's lanes,
 //   are summed over the group by halving: lanes exchange half of what they
 //   hold, and lane x ends with the sum of pair reversed(x) = key R + row.
-//   outputs: a lane's four columns of the R rows; the weights come by shuffle.
+//   outputs: a lane's four columns of the R rows; the weights go through
+//   shared memory, a group's own.
 constexpr int kFewRows = 8;
 
 template <int L>
@@ -89,12 +90,14 @@ __device__ __forceinline__ void few_rows(const Params& p, const Job& jb, float s
   constexpr int DP = D + 4, L = D / 4, NG = kSimtThreads / L, IT = 64 / NG, KB = L / R, NB = IT / KB;
   static_assert(KB * R == L && NB * KB == IT, "a batch of keys fills the group");
   static_assert((size_t)NG * R * D <= 2 * 64 * DP && NG * R * 2 <= 64 * DP, "the groups' states fit the tiles");
+  static_assert(R <= 16 && 16 * DP + 64 * R <= 64 * DP, "the weights fit behind the queries");
   const int tid = threadIdx.x, x = tid % L, grp = tid / L, e0 = 4 * x;
   // this lane's pair: row and key of a batch
   const int pair = (int)(__brev((unsigned)x) >> (L == 32 ? 27 : 28)), prow = pair % R, pkey = pair / R;
   auto row_last = [&](int r) { return jb.p0 + p.by_group.div(jb.r0 + r); };
   const int last = prow < jb.rv ? row_last(prow) : -1;
   auto sees = [&](int row_end, int key) { return key <= row_end && (p.window == 0 || key > row_end - p.window); };
+  float* weights = sq + 16 * DP + grp * (NB * L);   // the group's, behind the queries
   float q[R][4], o[R][4], m = -INFINITY, l = 0.f;
 #pragma unroll
   for (int r = 0; r < R; ++r)
@@ -124,11 +127,11 @@ __device__ __forceinline__ void few_rows(const Params& p, const Job& jb, float s
           v[k * R + r] = fmaf(q[r][0], y.x, fmaf(q[r][1], y.y, fmaf(q[r][2], y.z, q[r][3] * y.w)));
       }
 #pragma unroll
-      for (int o2 = 1, n = L / 2; o2 < L; o2 *= 2, n /= 2) {
+      for (int o2 = 1; o2 < L; o2 *= 2) {
         const bool upper = x & o2;
 #pragma unroll
-        for (int i = 0; i < n; ++i) {
-          const float give = upper ? v[i] : v[i + n], keep = upper ? v[i + n] : v[i];
+        for (int i = 0; i < L / 2 / o2; ++i) {
+          const float low = v[i], high = v[i + L / 2 / o2], give = upper ? low : high, keep = upper ? high : low;
           v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o2);
         }
       }
@@ -147,9 +150,11 @@ __device__ __forceinline__ void few_rows(const Params& p, const Job& jb, float s
     l *= f;
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-      s[b] = fast_exp2(s[b] - base);
-      l += s[b];
+      const float e = fast_exp2(s[b] - base);
+      weights[b * L + pair] = e;
+      l += e;
     }
+    __syncwarp();
     if (__any_sync(0xffffffffu, f != 1.f))
 #pragma unroll
       for (int r = 0; r < R; ++r) {
@@ -160,26 +165,40 @@ __device__ __forceinline__ void few_rows(const Params& p, const Job& jb, float s
     if (more) copies_wait<1>();                 // this lane's own part of V
     else copies_wait<0>();
 #pragma unroll
-    for (int b = 0; b < NB; ++b)
+    for (int b = 0; b < NB; ++b) {
+      float4 y[KB];
+      float big = 0.f;
 #pragma unroll
       for (int k = 0; k < KB; ++k) {
-        const int row = grp + NG * (b * KB + k);
-        const float4 y = *reinterpret_cast<const float4*>(sv + row * DP + e0);
-        float w[R];
-#pragma unroll
-        for (int r = 0; r < R; ++r) w[r] = __shfl_sync(0xffffffffu, s[b], reversed<L>(k * R + r), L);
-        // 0 times a value that is not finite is not 0: a key is left out for the rows that do not see it
-        const bool finite = fabsf(y.x) < INFINITY && fabsf(y.y) < INFINITY && fabsf(y.z) < INFINITY &&
-                            fabsf(y.w) < INFINITY;
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-          if (!finite && (r >= jb.rv || !sees(row_last(r), k0 + row))) continue;
-          o[r][0] = fmaf(w[r], y.x, o[r][0]);
-          o[r][1] = fmaf(w[r], y.y, o[r][1]);
-          o[r][2] = fmaf(w[r], y.z, o[r][2]);
-          o[r][3] = fmaf(w[r], y.w, o[r][3]);
-        }
+        y[k] = *reinterpret_cast<const float4*>(sv + (grp + NG * (b * KB + k)) * DP + e0);
+        // (0 or NaN)
+        big = fmaf(y[k].x, 0.f, fmaf(y[k].y, 0.f, fmaf(y[k].z, 0.f, fmaf(y[k].w, 0.f, big))));
       }
+      // 0 times a value that is not finite is not 0: where one was met, a key
+      // is left out for the rows that do not see it
+      auto product = [&](auto guarded) {
+#pragma unroll
+        for (int k = 0; k < KB; ++k) {
+          float4 four[R / 4];
+#pragma unroll
+          for (int r = 0; r < R; r += 4)
+            four[r / 4] = *reinterpret_cast<const float4*>(weights + b * L + k * R + r);
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            const float4 z = four[r / 4];
+            const float w = (r & 3) == 0 ? z.x : (r & 3) == 1 ? z.y : (r & 3) == 2 ? z.z : z.w;
+            if (decltype(guarded)::value &&
+                (r >= jb.rv || !sees(row_last(r), k0 + grp + NG * (b * KB + k)))) continue;
+            o[r][0] = fmaf(w, y[k].x, o[r][0]);
+            o[r][1] = fmaf(w, y[k].y, o[r][1]);
+            o[r][2] = fmaf(w, y[k].z, o[r][2]);
+            o[r][3] = fmaf(w, y[k].w, o[r][3]);
+          }
+        }
+      };
+      if (__any_sync(0xffffffffu, big != 0.f)) product(std::true_type{});
+      else product(std::false_type{});
+    }
     __syncwarp();
     if (more) issue(k0 + 64, Vc, sv);
   }
@@ -203,7 +222,6 @@ __device__ __forceinline__ void few_rows(const Params& p, const Job& jb, float s
 #pragma unroll
   for (int g = 0; g < NG; ++g) {
     const float2 y = ml[g * R + r];
-    if (y.y == 0.f) continue;                   // no key of the row with this group
     const float f = fast_exp2(y.x - base);
     const float4 v = *reinterpret_cast<const float4*>(sk + (g * R + r) * D + e0);
     sum = fmaf(y.y, f, sum);
@@ -542,6 +560,8 @@ paged_combine_kernel(Params p, Workspace ws, T* __restrict__ O) {
       for (int j = 0; j < 2; ++j) {
         const int k = k0 + j * step;
         ml[j] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[j][e] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (k >= n) continue;
         ml[j] = ws.state(slots[k])[r];
 #pragma unroll
@@ -559,9 +579,9 @@ paged_combine_kernel(Params p, Workspace ws, T* __restrict__ O) {
       for (int e = 0; e < 16; ++e) acc[e] *= f0;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        // no visible key in this portion, or no portion; the sum tells, for the
-        // maximum of scores that are all NaN is -inf as well
-        if (ml[j].y == 0.f) continue;
+        // (a portion without a visible key adds zeros: nothing is left out, since
+        // scores that are all NaN leave a maximum of -inf, and weights of 0 an
+        // output that is NaN where a value is infinite)
         const float f = fast_exp2(ml[j].x - base);
         sum = fmaf(ml[j].y, f, sum);
 #pragma unroll
@@ -587,13 +607,12 @@ paged_combine_kernel(Params p, Workspace ws, T* __restrict__ O) {
     for (int k = 1; k < step; ++k) M = M < red[tid + k * rows][0] || red[tid + k * rows][0] != red[tid + k * rows][0]
                                            ? red[tid + k * rows][0] : M;
     const float base = M == -INFINITY ? 0.f : M;
-    const float f0 = m == -INFINITY ? 0.f : fast_exp2(m - base);
+    const float f0 = fast_exp2(m - base);
     sum *= f0;
 #pragma unroll
     for (int e = 0; e < 16; ++e) acc[e] *= f0;
     for (int k = 1; k < step; ++k) {
       const float* x = red[tid + k * rows];
-      if (x[1] == 0.f) continue;
       const float f = fast_exp2(x[0] - base);
       sum = fmaf(x[1], f, sum);
 #pragma unroll

@@ -195,6 +195,25 @@ def test_values_of_unseen_new_tokens(lib, dtype, d, Hq, bad):
     assert not np.isfinite(hit).any() and (np.isnan(hit).all() if math.isnan(bad) else (hit == bad).all())
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("group", [1, 2, 4])
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+def test_values_of_an_unseen_second_token(lib, dtype, group, bad):
+    # two tokens in one item: the first row does not see the second's key, whose K and V are not finite
+    c = Case([130, 63], [2, 2], 2 * group, 2, 128, 16, dtype, seed=22)
+    before = c.oracle()
+    for s, at in ((0, 131), (1, 64)):
+        c.Vc[c.table[s, at // 16], :, at % 16] = bad
+        c.Kc[c.table[s, at // 16], :, at % 16, 3] = bad
+    out = c.run()
+    torch.cuda.synchronize()
+    assert_no_device_error()
+    got, (O, A, _) = np64(out), before
+    assert not np.isfinite(got[[1, 3]]).any()
+    bound = (2.0 ** -8 + 2e-4) * A + 2.0 ** -7 * np.abs(O) + 1e-6
+    assert (np.abs(got - O) <= bound)[[0, 2]].all()
+
+
 @pytest.mark.parametrize("dtype,Hq,Hkv", [(BF, 16, 2), (BF, 3, 1), (F32, 4, 2)])
 def test_long_contexts_split_over_many_ctas(lib, dtype, Hq, Hkv):
     # few rows and many keys: every item is split, and merged in key order
