@@ -20,13 +20,15 @@ using namespace paged;
 // its 16 tx lanes, in 32 bits as the products are.  K and V of a tile come by
 // cp.async, both before the scores, and the scores' exponentials take K's
 // place, so that two CTAs fit an SM and one's loads run beside the other's
-// products.  Bound by the FMA pipe for prompts; items of up to 16 rows
-// (decoding) form only the row group i = 0.
+// products.  Prompts are bound by shared memory's rate and the FMA pipe beside
+// it (64 x 64 x 64 products in 2800 cycles an SM, 2048 at the FMA rate); items
+// of 9 to 16 rows form only the row group i = 0, smaller ones take few_rows.
 constexpr int kSimtThreads = 256;
 constexpr int kSimtRows = 64;
 struct SimtTiling {
   static constexpr int BN = 64;
-  // a tile of at most 16 rows (a half item here) costs its loads, about half a full tile
+  // a tile of at most 16 rows (a half item here) costs about half a full tile
+  // (for those of up to 8 rows 1, 2 and 3 measured alike)
   static constexpr int kUnit = 4, kUnitHalf = 2, kOver = 2, kMinShare = 4;
 };
 constexpr int kPitchP = 68;
