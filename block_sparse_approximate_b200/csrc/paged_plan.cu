@@ -303,9 +303,13 @@ extern "C" sa_status sa_paged_plan(const int32_t* ctx_len, const int32_t* new_le
   const int threads = work <= 256 ? 256 : shape.S <= 512 ? 512 : 1024;
   int ctas = 1;
   while (ctas < kPlanMaxCluster && ctas * 1024 < work) ctas *= 2;
-  const size_t smem = (size_t)shape.S * 5 * sizeof(int);
-  if (smem > 48 * 1024 &&
-      cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+  // Static arrays count towards the 48 KB that a CTA has by default, so the
+  // opt-in is taken well before the sums alone fill it; always to the same
+  // size, since the attribute is shared by all threads that call.
+  constexpr int kSums = 5 * sizeof(int), kMostSmem = paged::kMaxRequests * kSums;
+  const size_t smem = (size_t)shape.S * kSums;
+  if (smem > 40 * 1024 && cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               kMostSmem) != cudaSuccess)
     return launch_status("cudaFuncSetAttribute(paged_plan_kernel)");
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas);
