@@ -507,7 +507,9 @@ def paged_plan(ctx_len: torch.Tensor, new_len: torch.Tensor, held: torch.Tensor,
     lengths (int32 [S]): updates held [S], table [S,max_pages], free_pages [P]
     and free_state [2] (all int32) in place and returns (q_start int32 [S+1],
     kv_len int32 [S], slots int64 [tokens]).  ``tokens``: rows of the step's
-    packed arrays, padding included.  See sa_paged_plan for refused requests."""
+    packed arrays, padding included.  None of the arrays that are written may
+    overlap another (SparseAttnError): the lengths are the caller's own
+    tensors.  See sa_paged_plan for refused requests."""
     (S,), (P,), (rows, width) = ctx_len.shape, free_pages.shape, table.shape
     if rows != S or new_len.shape != (S,) or held.shape != (S,) or free_state.shape != (2,):
         raise ValueError("new_len and held must be [S], table [S, max_pages], free_state [2]")

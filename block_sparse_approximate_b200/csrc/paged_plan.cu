@@ -196,7 +196,8 @@ paged_plan_kernel(const int32_t* __restrict__ ctx_len, const int32_t* __restrict
   else __syncthreads();
   if (rank == 0) {
     for (int s = tid; s < S; s += nthr)
-      if (owned[s] >= 0) held[s] = (int)(((int64_t)ctx_len[s] + new_len[s] + page - 1) >> page_shift);
+      if (owned[s] >= 0)
+        held[s] = owned[s] + (ask_end[s] - (s ? ask_end[s - 1] : 0)) - (give_end[s] - (s ? give_end[s - 1] : 0));
     if (tid == 0) {
       free_state[0] = ring_at(taken);
       free_state[1] = min(count - taken + given, P);
@@ -295,6 +296,30 @@ extern "C" sa_status sa_paged_plan(const int32_t* ctx_len, const int32_t* new_le
       return fail(SA_ERR_ALIGNMENT, "sa_paged_plan: 32-bit arrays must be 4-byte aligned");
   if (reinterpret_cast<uintptr_t>(slots) & 7u)
     return fail(SA_ERR_ALIGNMENT, "sa_paged_plan: slots must be 8-byte aligned");
+  // The call rewrites its state in place and reads the lengths from several
+  // CTAs: an array that is written is no other's memory (kv_len as the next
+  // step's ctx_len would be).
+  const size_t n = (size_t)shape.S * 4;
+  const struct {
+    const char* name;
+    const void* at;
+    size_t bytes;
+  } arrays[] = {{"slots", slots, (size_t)shape.T * 8},
+                {"kv_len", kv_len, n},
+                {"q_start", q_start, n + 4},
+                {"free_state", free_state, 8},
+                {"free_pages", free_pages, (size_t)shape.P * 4},
+                {"table", table, n * shape.max_pages},
+                {"held", held, n},
+                {"new_len", new_len, n},
+                {"ctx_len", ctx_len, n}};
+  for (int a = 0; a < 7; ++a)
+    for (int b = a + 1; b < 9; ++b) {
+      const uintptr_t x = reinterpret_cast<uintptr_t>(arrays[a].at), y = reinterpret_cast<uintptr_t>(arrays[b].at);
+      if (x < y + arrays[b].bytes && y < x + arrays[a].bytes)
+        return fail(SA_ERR_INVALID_ARG,
+                    std::string("sa_paged_plan: ") + arrays[a].name + " and " + arrays[b].name + " overlap");
+    }
   // One CTA up to 1024 rows and requests, from there a cluster of a power of
   // two up to 8; 512 threads each (8.4 us for 512 requests and 32615 rows,
   // with 1024 threads, whose scan has twice the warps, 9.4; 4 CTAs 11.4) and

@@ -186,7 +186,11 @@ class PagedServing:
         self.out = torch.zeros(tokens, Hq, d, device=dev, dtype=dtype)
 
     def plan(self, ctx_len, new_len, stream=None):
-        """Pages and slots for new_len[s] more tokens of each request (see binding.paged_plan)."""
+        """Pages and slots for new_len[s] more tokens of each request (see binding.paged_plan).
+
+        The call writes ``self.kv_len``, so ctx_len is a tensor of the caller's own: what it knows of the
+        requests' lengths, or a copy of kv_len once no request was refused (a refused one's kv_len is 0).
+        """
         return bd.paged_plan(ctx_len, new_len, self.held, self.table, self.free_pages, self.free_state, self.tokens,
                              self.page, q_start=self.q_start, kv_len=self.kv_len, slots=self.slots, stream=stream)
 

@@ -460,10 +460,12 @@ typedef struct {
  * max_pages pages, when its rows end behind T, or when the pages asked for up
  * to and including it (refused ones too) are more than the free ones; its
  * pages, its table row and held[s] stay as they are, and its rows keep their
- * places in q_start.  Hq, Hkv and d of the shape are not used.  The arrays
- * must not overlap.
- * Errors: SA_ERR_INVALID_ARG (S, P or max_pages not positive, a null array),
- *         SA_ERR_UNSUPPORTED, SA_ERR_ALIGNMENT (element alignment). */
+ * places in q_start.  Hq, Hkv and d of the shape are not used.  No array that
+ * is written may overlap another one: the kv_len of one step, copied, can be
+ * the ctx_len of the next (0, which ends the request, where it was refused).
+ * Errors: SA_ERR_INVALID_ARG (S, P or max_pages not positive, a null array,
+ *         arrays that overlap), SA_ERR_UNSUPPORTED, SA_ERR_ALIGNMENT (element
+ *         alignment). */
 sa_status sa_paged_plan(const int32_t* ctx_len, const int32_t* new_len, sa_paged_shape shape, int32_t* held,
                         int32_t* table, int32_t* free_pages, int32_t* free_state, int32_t* q_start,
                         int32_t* kv_len, int64_t* slots, void* stream);

@@ -183,3 +183,22 @@ def test_binding_refuses_host_tensors_and_wrong_layouts():
     for window in (-1, 1 << 31, (1 << 32) + 5):
         with pytest.raises(ValueError, match="window"):
             bd.paged_attn_fwd(x, c, c, i(2, 3), i(3), i(2), 1.0, window=window)
+
+
+def test_plan_refuses_arrays_that_overlap(lib):
+    # the lengths that a call writes are not those that it reads: every pair of arrays of which one is written
+    S, T, P, width = 8, 32, 64, 4
+    sizes = dict(ctx=4 * S, new=4 * S, held=4 * S, table=4 * S * width, ring=4 * P, state=8, q_start=4 * (S + 1),
+                 kv_len=4 * S, slots=8 * T)
+    sh = bd.PagedShape(S=S, T=T, Hq=1, Hkv=1, d=64, page=16, P=P, max_pages=width)
+    names = list(sizes)
+    for a in names:
+        for b in names:
+            if a == b or {a, b} == {"ctx", "new"}:
+                continue
+            at = {n: FAKE + 0x1000 * k for k, n in enumerate(names)}
+            for shift in (0, (sizes[a] - 1) // 8 * 8 if b == "slots" else sizes[a] - 4):
+                at[b] = at[a] + shift              # b begins with a, or within its last elements
+                status = lib.sa_paged_plan(at["ctx"], at["new"], sh, *(at[n] for n in names[2:]), None)
+                assert status == bd.SA_ERR_INVALID_ARG, (a, b, shift)
+                assert "overlap" in lib.sa_last_error().decode(), (a, b)
