@@ -13,6 +13,7 @@ from __future__ import annotations
 import argparse
 import glob
 import os
+import re
 import subprocess
 import sys
 from concurrent.futures import ThreadPoolExecutor
@@ -43,22 +44,27 @@ def _headers():
 # must cover the split (256 x 216 + 128 x 40, and 128 x 216 + 128 x 96 +
 # 128 x 56, see attn_tc.cu; 256 x 216 + 128 x 72, see paged_attn_tc.cu), or
 # setmaxnreg.inc would wait for registers that never come.
-TC_MIN_LAUNCH_REGS = {"attn_tc.cu": 158, "paged_attn_tc.cu": 168}
+TC_MIN_LAUNCH_REGS = {"attn_tc.cu": {"attn_tc_kernel": 158, "attn_tc_linmix_kernel": 158},
+                      "paged_attn_tc.cu": {"paged_attn_tc_kernel": 168}}
 
 
-def _check_tc_registers(ptxas_log: str, least: int):
-    import re
+def _check_tc_registers(source: str, ptxas_log: str):
+    """Raises unless the log shows every guarded kernel of ``source`` with enough registers."""
     lines = ptxas_log.splitlines()
-    for k, line in enumerate(lines):
-        if "Compiling entry function" in line and ("attn_tc_kernel" in line or "attn_tc_linmix_kernel" in line):
-            for nxt in lines[k + 1:k + 4]:
-                m = re.search(r"Used (\d+) registers", nxt)
-                if m:
-                    regs = int(m.group(1))
-                    if regs < least:
-                        raise RuntimeError(f"attn_tc_kernel launches with {regs} registers per thread; "
-                                           f"the setmaxnreg split needs >= {least}")
-                    break
+    for kernel, least in TC_MIN_LAUNCH_REGS[source].items():
+        checked = 0
+        for k, line in enumerate(lines):
+            if "Compiling entry function" not in line or f"{len(kernel)}{kernel}" not in line:
+                continue
+            found = re.search(r"Used (\d+) registers", "\n".join(lines[k + 1:k + 4]))
+            if not found:
+                raise RuntimeError(f"{source}: the ptxas output gives no register count for {kernel}")
+            if int(found.group(1)) < least:
+                raise RuntimeError(f"{source}: {kernel} launches with {found.group(1)} registers per thread; "
+                                   f"the setmaxnreg split needs >= {least}")
+            checked += 1
+        if not checked:
+            raise RuntimeError(f"{source}: the ptxas output does not show {kernel}")
 
 
 def _stale(target, deps):
@@ -79,24 +85,31 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             extra = list(extra_flags)
             if os.path.basename(src) in TC_MIN_LAUNCH_REGS and "-v" not in extra:
                 extra += ["-Xptxas", "-v"]
-            cmd = [NVCC, *ARCH, *FLAGS, *extra, "-c", src, "-o", obj]
-            jobs.append(cmd)
+            jobs.append((src, obj, [NVCC, *ARCH, *FLAGS, *extra, "-c", src, "-o", obj[:-2] + ".tmp.o"]))
 
-    def run(cmd):
+    # An object takes its name once it has passed the check, so that a kernel
+    # that fails it is compiled and refused again by the next build.
+    def run(job):
+        src, obj, cmd = job
         if verbose:
             print(" ".join(cmd), flush=True)
         r = subprocess.run(cmd, capture_output=True, text=True)
-        return cmd, r
+        log = r.stdout + r.stderr
+        if verbose and log:
+            print(log, flush=True)
+        try:
+            if r.returncode != 0:
+                raise RuntimeError("nvcc failed:\n" + " ".join(cmd) + "\n" + log)
+            if os.path.basename(src) in TC_MIN_LAUNCH_REGS:
+                _check_tc_registers(os.path.basename(src), log)
+            os.replace(cmd[-1], obj)
+        finally:
+            if os.path.exists(cmd[-1]):
+                os.remove(cmd[-1])
 
     with ThreadPoolExecutor(max_workers=min(8, max(1, len(jobs)))) as ex:
-        for cmd, r in ex.map(run, jobs):
-            if verbose and (r.stdout or r.stderr):
-                print(r.stdout + r.stderr, flush=True)
-            if r.returncode != 0:
-                raise RuntimeError("nvcc failed:\n" + " ".join(cmd) + "\n" + r.stdout + r.stderr)
-            least = TC_MIN_LAUNCH_REGS.get(os.path.basename(cmd[-3]))
-            if least is not None:
-                _check_tc_registers(r.stdout + r.stderr, least)
+        for _ in ex.map(run, jobs):
+            pass
     if force or jobs or _stale(LIB, objs):
         cmd = [NVCC, *ARCH, "-shared", "-o", LIB, *objs]
         r = subprocess.run(cmd, capture_output=True, text=True)
