@@ -731,8 +731,9 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
               mx8[e & 7] = fmax3_nan(mx8[e & 7], __uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
             const float mx = fmax3_nan(fmax3_nan(mx8[0], mx8[1], mx8[2]), fmax3_nan(mx8[3], mx8[4], mx8[5]),
                                        fmax3_nan(mx8[6], mx8[7], mx8[7]));
-            // a score that is NaN or +inf makes the row NaN (as inf - inf does)
-            const float m_tile = mx < INFINITY ? mx * scale2 : NAN;
+            // a score that is NaN or +inf makes the row NaN (as inf - inf does),
+            // whether q.k is so or the scale takes it there
+            const float top = mx * scale2, m_tile = top < INFINITY ? top : NAN;
             need = !(m_tile <= m_used + kLazy);
             if (need) {
               factor = fast_exp2(m_used - m_tile);

@@ -493,9 +493,10 @@ size_t sa_paged_attn_workspace_size(sa_paged_shape shape);
  * head h reads KV head h / (Hq / Hkv):
  *   o = sum e^{scale q.k} v / sum e^{scale q.k}   over the keys it sees,
  * 0 for a row that sees none (kv_len[s] < n - i; a refused request).  scale
- * is positive and finite.  One
- * row per request is decoding, several are a chunk of a prompt, and a call
- * may mix them.  Q: [T,Hq,d] with row stride q_row_stride (elements), the
+ * is positive and finite.  Scores are float32: one that is NaN or +inf there
+ * makes its row NaN, and a row whose scores are all -inf is 0.  One row per
+ * request is decoding, several are a chunk of a prompt, and a call may mix
+ * them.  Q: [T,Hq,d] with row stride q_row_stride (elements), the
  * heads of a row contiguous; O: [T,Hq,d] contiguous; rows from q_start[S] on
  * are left as they were.  Q, caches and O of `dtype`: bf16 runs on the tensor
  * cores (p rounded to bf16 for the second product), fp32 on CUDA cores; maxima,

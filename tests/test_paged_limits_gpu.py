@@ -11,7 +11,8 @@ import torch
 import oracle
 from block_sparse_approximate_b200 import binding as bd
 from block_sparse_approximate_b200.pipeline import PagedServing
-from tests.test_paged_gpu import DEV, _i32
+from tests._parity import assert_no_device_error, np64
+from tests.test_paged_gpu import BF, DEV, F32, Case, _i32, assert_attention
 
 pytestmark = pytest.mark.gpu
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -76,3 +77,48 @@ def test_plan_of_adjacent_arrays(lib, S, tokens):
     for x, y in zip((q_start, kv_len, slots, held, table, ring, state), ref):
         np.testing.assert_array_equal(x.cpu().numpy(), y)
     assert ctx_d.count_nonzero() == 0 and np.array_equal(new_d.cpu().numpy(), new)
+
+
+def planted(c, s, key):
+    """The pool's page and offset of a request's key."""
+    page = c.Kc.shape[2]
+    return int(c.table[s, key // page]), key % page
+
+
+@pytest.mark.parametrize("dtype,d,Hq", [(BF, 128, 8), (BF, 64, 2), (F32, 128, 8), (F32, 64, 2), (F32, 64, 16)])
+@pytest.mark.parametrize("n", [1, 3, 70])
+def test_scores_above_float32(lib, dtype, d, Hq, n):
+    # q.k is finite and scale q.k is not: such a row is NaN, wherever the key lies; the other KV head's scores are 0
+    c = Case([300, 40, 2000], [n, n, n], Hq, 2, d, 32, dtype, seed=31, poison=False)
+    c.scale = 8.0
+    c.Q = torch.zeros_like(c.Q)
+    c.Q[..., 0] = 2.0 ** 63
+    c.Kc[..., 0] = 0.0
+    for s, key in ((0, 5), (1, 40), (2, 1500)):
+        pid, off = planted(c, s, key)
+        c.Kc[pid, 0, off, 0] = 2.0 ** 63
+    out = c.run()
+    torch.cuda.synchronize()
+    assert_no_device_error()
+    assert out[:, :Hq // 2].isnan().all()
+    c.Kc[..., 0] = 0.0                             # (the oracle has no such rows; weights are equal and exact)
+    O, A, seen = c.oracle()
+    w = 2.0 ** -8 if dtype == BF else 2.0 ** -24   # the weight's and the output's rounding
+    bound = (w + 2 * (2.0 ** -21 + seen[:, None, None] * 2.0 ** -24)) * A + 2 * w * np.abs(O)
+    assert (np.abs(np64(out) - O) <= bound)[:, Hq // 2:].all()
+
+
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (BF, 64), (F32, 128), (F32, 64)])
+@pytest.mark.parametrize("n", [1, 5, 40])
+def test_rows_whose_scores_are_all_minus_infinity(lib, dtype, d, n):
+    # one KV head's keys score -inf (K holds it): its rows are zero, the other head's are as ever
+    c = Case([200, 2500, 3], [n, n, n], 4, 2, d, 16, dtype, seed=33, poison=False)
+    c.Q = c.Q.clone()
+    c.Q[..., 0] = 1.0
+    O, A, seen = c.oracle()
+    c.Kc[:, 1, :, 0] = float("-inf")
+    out = c.run(out=torch.full((c.T, 4, d), 7.0, device=DEV, dtype=dtype))
+    assert (out[:, 2:] == 0).all()
+    c.Kc[:, 1, :, 0] = 0.0
+    out[:, 2:] = torch.from_numpy(O[:, 2:]).to(DEV).to(dtype)
+    assert_attention(out, O, A, seen, c, 7.0)
