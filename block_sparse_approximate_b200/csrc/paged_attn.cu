@@ -696,8 +696,8 @@ extern "C" sa_status sa_paged_attn_fwd(const void* Q, int64_t q_row_stride, cons
   sa_status r = check_attn_shape(shape, dtype, "sa_paged_attn_fwd");
   if (r != SA_OK) return r;
   if (window < 0) return fail(SA_ERR_INVALID_ARG, "sa_paged_attn_fwd: window must be 0 (none) or positive");
-  if (!(scale > 0.f && scale < INFINITY))
-    return fail(SA_ERR_INVALID_ARG, "sa_paged_attn_fwd: scale must be positive and finite");
+  if (!(scale > 0.f && scale * kLog2e < INFINITY))   // (the kernels' scores are in powers of 2)
+    return fail(SA_ERR_INVALID_ARG, "sa_paged_attn_fwd: scale must be positive, and scale * log2(e) finite");
   if (shape.T == 0 || shape.S == 0) return SA_OK;   // no row belongs to a request
   if (!Q || !q_start || !kv_len || !O || (shape.P > 0 && shape.max_pages > 0 && (!Kcache || !Vcache || !table)))
     return fail(SA_ERR_INVALID_ARG, "sa_paged_attn_fwd: Q, caches, q_start, kv_len, table and O are required");

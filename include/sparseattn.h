@@ -493,24 +493,24 @@ size_t sa_paged_attn_workspace_size(sa_paged_shape shape);
  * head h reads KV head h / (Hq / Hkv):
  *   o = sum e^{scale q.k} v / sum e^{scale q.k}   over the keys it sees,
  * 0 for a row that sees none (kv_len[s] < n - i; a refused request).  scale
- * is positive and finite.  Scores are float32: one that is NaN or +inf there
- * makes its row NaN, and a row whose scores are all -inf is 0.  One row per
- * request is decoding, several are a chunk of a prompt, and a call may mix
- * them.  Q: [T,Hq,d] with row stride q_row_stride (elements), the
+ * is positive and scale log2(e) finite.  Scores are float32: one that is NaN
+ * or +inf there makes its row NaN, and a row whose scores are all -inf is 0.
+ * One row per request is decoding, several are a chunk of a prompt, and a call
+ * may mix them.  Q: [T,Hq,d] with row stride q_row_stride (elements), the
  * heads of a row contiguous; O: [T,Hq,d] contiguous; rows from q_start[S] on
  * are left as they were.  Q, caches and O of `dtype`: bf16 runs on the tensor
- * cores (p rounded to bf16 for the second product), fp32 on CUDA cores; maxima,
- * sums and outputs are held in float32.  A key that no row of a request sees
- * (behind kv_len, left of the window) is never used, whatever its memory
- * holds, and a key that a row does not see does not reach that row, also
- * where its K or V is not finite.  A table entry outside [0, P) under a
+ * cores (p rounded to bf16 for the second product), fp32 on CUDA cores;
+ * maxima, sums and outputs are held in float32.  A key that no row of a
+ * request sees (behind kv_len, left of the window) is never used, whatever its
+ * memory holds, and a key that a row does not see does not reach that row,
+ * also where its K or V is not finite.  A table entry outside [0, P) under a
  * visible key makes that request's output unspecified.  q_start is read as
  * q_start[s] clamped to [0, T], kv_len to [0, max_pages * page]; requests
- * whose row ranges overlap leave either one's output.  workspace:
- * at least sa_paged_attn_workspace_size() bytes, 256-byte aligned, contents
- * on entry do not matter; calls that may run at the same time need one each.
- * O and the workspace overlap no other array.
- * The result does not depend on scheduling (no atomics).
+ * whose row ranges overlap leave either one's output.  workspace: at least
+ * sa_paged_attn_workspace_size() bytes, 256-byte aligned, contents on entry do
+ * not matter; calls that may run at the same time need one each.  O and the
+ * workspace overlap no other array.  The result does not depend on scheduling
+ * (no atomics).
  * Errors: SA_ERR_INVALID_ARG, SA_ERR_UNSUPPORTED, SA_ERR_ALIGNMENT,
  *         SA_ERR_WORKSPACE. */
 sa_status sa_paged_attn_fwd(const void* Q, int64_t q_row_stride, const void* Kcache, const void* Vcache,

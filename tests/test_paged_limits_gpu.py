@@ -122,3 +122,10 @@ def test_rows_whose_scores_are_all_minus_infinity(lib, dtype, d, n):
     c.Kc[:, 1, :, 0] = 0.0
     out[:, 2:] = torch.from_numpy(O[:, 2:]).to(DEV).to(dtype)
     assert_attention(out, O, A, seen, c, 7.0)
+
+
+def test_scale_whose_logarithm_base_2_overflows_is_refused(lib):
+    c = Case([5], [1], 2, 1, 64, 16, BF, seed=32, poison=False)
+    c.scale = 3e38
+    with pytest.raises(bd.SparseAttnError, match="scale"):
+        c.run()

@@ -202,3 +202,13 @@ def test_plan_refuses_arrays_that_overlap(lib):
                 status = lib.sa_paged_plan(at["ctx"], at["new"], sh, *(at[n] for n in names[2:]), None)
                 assert status == bd.SA_ERR_INVALID_ARG, (a, b, shift)
                 assert "overlap" in lib.sa_last_error().decode(), (a, b)
+
+
+def test_attention_refuses_a_scale_that_overflows_in_base_2(lib):
+    # (without a workspace, so that no call gets as far as a launch)
+    sh = bd.PagedShape(S=4, T=8, Hq=8, Hkv=4, d=128, page=16, P=32, max_pages=4)
+    for dtype in (0, 1):
+        for scale, status in ((2.3e38, bd.SA_ERR_WORKSPACE), (2.4e38, bd.SA_ERR_INVALID_ARG),
+                              (3.4e38, bd.SA_ERR_INVALID_ARG)):
+            assert lib.sa_paged_attn_fwd(FAKE, 1024, FAKE, FAKE, dtype, sh, FAKE, FAKE, FAKE, 0, scale, FAKE, None, 0,
+                                         None) == status, scale
