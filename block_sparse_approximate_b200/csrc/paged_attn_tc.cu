@@ -34,7 +34,9 @@
 // is not 0, the values of an edge tile (one that some row of the item does
 // not see whole) are screened before P V: rows of V outside the item's span
 // are cleared, and elements that are not finite are cleared and added back
-// after the item's store for the rows that see them (add_unbounded).
+// after the item's store for the rows that see them (add_unbounded), whatever
+// their weights: an infinite value whose weight is 0 in float32 gives its
+// infinity there and NaN in a tile that is seen whole, never a finite output.
 #include "paged.cuh"
 #include "tc_util.cuh"
 

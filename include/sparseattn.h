@@ -503,10 +503,14 @@ size_t sa_paged_attn_workspace_size(sa_paged_shape shape);
  * maxima, sums and outputs are held in float32.  A key that no row of a
  * request sees (behind kv_len, left of the window) is never used, whatever its
  * memory holds, and a key that a row does not see does not reach that row,
- * also where its K or V is not finite.  A table entry outside [0, P) under a
- * visible key makes that request's output unspecified.  q_start is read as
- * q_start[s] clamped to [0, T], kv_len to [0, max_pages * page]; requests
- * whose row ranges overlap leave either one's output.  workspace: at least
+ * also where its K or V is not finite.  A value that is not finite, of a key
+ * that a row does see, makes that column of the row not finite: an infinite
+ * one gives its infinity or NaN where its weight is so small that float32
+ * takes it for 0 in some tile (0 times infinity), and which of the two is not
+ * specified.  A table entry outside [0, P) under a visible key makes that
+ * request's output unspecified.  q_start is read as q_start[s] clamped to
+ * [0, T], kv_len to [0, max_pages * page]; requests whose row ranges overlap
+ * leave either one's output.  workspace: at least
  * sa_paged_attn_workspace_size() bytes, 256-byte aligned, contents on entry do
  * not matter; calls that may run at the same time need one each.  O and the
  * workspace overlap no other array.  The result does not depend on scheduling

@@ -1,4 +1,5 @@
 """The paged KV cache at its limits on the GPU, against the float64 oracle."""
+import math
 import os
 import subprocess
 import sys
@@ -129,3 +130,43 @@ def test_scale_whose_logarithm_base_2_overflows_is_refused(lib):
     c.scale = 3e38
     with pytest.raises(bd.SparseAttnError, match="scale"):
         c.run()
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+@pytest.mark.parametrize("low", [-1e4, float("-inf")])
+@pytest.mark.parametrize("dtype,d,lens", [
+    (BF, 128, "whole"), (BF, 64, "split"), (BF, 128, "split"), (BF, 128, "chunk"), (BF, 64, "chunk"),
+    (F32, 64, "whole"), (F32, 128, "split"), (F32, 64, "chunk")])
+def test_values_under_vanishing_weights(lib, dtype, d, lens, low, bad):
+    # A key that rows see with a weight of 0 holds a value that is not finite: its column is not finite, whether
+    # the key's tile is seen whole (5, 130) or in part (the last keys), in whole items, split ones and chunks
+    ctx, new = {"whole": ([260] * 300, [1] * 300), "split": ([9000, 700], [1, 2]),
+                "chunk": ([300, 0], [150, 200])}[lens]
+    c = Case(ctx, new, 4, 2, d, 16, dtype, seed=34, poison=False)
+    c.Q = c.Q.clone()
+    c.Q[..., 0] = 8.0
+    clean = c.Kc.clone()
+    keys = {0: (5, 130), 1: (c.kv[1] - 1,)}
+    hit = np.zeros(c.T, bool)
+    for s, at in keys.items():
+        for key in at:
+            pid, off = planted(c, s, key)
+            c.Kc[pid, :, off, 0] = low
+            first = c.kv[s] - new[s]
+            hit[c.q_start[s] + max(0, key - first):c.q_start[s + 1]] = True
+    # every row keeps a key of its own beside the planted ones
+    O, A, seen = c.oracle()
+    for s, at in keys.items():
+        for key in at:
+            pid, off = planted(c, s, key)
+            c.Vc[pid, :, off, 9] = bad
+    out = c.run()
+    torch.cuda.synchronize()
+    assert_no_device_error()
+    assert not out[torch.from_numpy(hit).to(DEV)][..., 9].isfinite().any()
+    if math.isnan(bad):
+        assert out[torch.from_numpy(hit).to(DEV)][..., 9].isnan().all()
+    want = torch.from_numpy(O).to(DEV).to(dtype)
+    out[torch.from_numpy(hit).to(DEV), :, 9] = want[torch.from_numpy(hit).to(DEV), :, 9]
+    c.Kc = clean                                   # (the largest score that counts is one of these)
+    assert_attention(out, O, A, seen, c, 7.0)
