@@ -1,4 +1,8 @@
-"""The paged KV cache at its limits on the GPU, against the float64 oracle."""
+"""The paged KV cache at its limits on the GPU, against the float64 oracle.
+
+Tolerances are those of test_paged_gpu's assert_attention, for fp32 too where
+masked keys are not finite, unless a test derives its own.
+"""
 import math
 import os
 import subprocess
@@ -170,3 +174,90 @@ def test_values_under_vanishing_weights(lib, dtype, d, lens, low, bad):
     out[torch.from_numpy(hit).to(DEV), :, 9] = want[torch.from_numpy(hit).to(DEV), :, 9]
     c.Kc = clean                                   # (the largest score that counts is one of these)
     assert_attention(out, O, A, seen, c, 7.0)
+
+
+@pytest.mark.parametrize("dtype,d,group", [(F32, 128, 1), (F32, 128, 2), (F32, 64, 4), (F32, 64, 1), (F32, 128, 4),
+                                           (BF, 128, 4), (BF, 64, 1)])
+@pytest.mark.parametrize("window", [0, 1, 70, 200])
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+def test_masked_keys_that_are_not_finite(lib, dtype, d, group, window, bad):
+    # K and V of some keys are not finite: rows that do not see them (earlier tokens; with a window also later ones)
+    # are right to the type's own tolerance, rows that see them are not finite
+    c = Case([200, 130, 63, 500, 260], [2, 3, 40, 130, 8], 2 * group, 2, d, 16, dtype, seed=35, window=window, pad=1)
+    out = torch.full((c.T, 2 * group, d), 7.0, device=DEV, dtype=dtype)
+    O, A, seen = c.oracle()
+    clean = c.Kc.clone()
+    hit = np.zeros(c.T, bool)
+    for s, back in enumerate((0, 1, 20, 64, 3)):   # the key is `back` tokens before the request's last
+        key = int(c.kv[s]) - 1 - back
+        pid, off = planted(c, s, key)
+        c.Vc[pid, :, off] = bad
+        c.Kc[pid, :, off, 3] = bad
+        first = key - (int(c.kv[s]) - (c.q_start[s + 1] - c.q_start[s]))
+        rows = np.arange(c.q_start[s + 1] - c.q_start[s])
+        hit[c.q_start[s]:c.q_start[s + 1]] = (rows >= first) & ((window == 0) | (rows < first + window))
+    c.run(out=out)
+    torch.cuda.synchronize()
+    assert_no_device_error()
+    mask = torch.from_numpy(hit).to(DEV)
+    assert not out[mask].isfinite().any()
+    out[mask] = torch.from_numpy(O).to(DEV).to(dtype)[mask]
+    c.Kc = clean
+    assert_attention(out, O, A, seen, c, 7.0)
+
+
+def test_serving_steps_in_fp32_are_close(lib):
+    # chunks, single tokens, a step back and a refused request, each step to fp32's tolerance
+    r = np.random.RandomState(36)
+    Hq, Hkv, d, page, T = 6, 2, 64, 16, 80
+    eng = PagedServing(requests=3, max_pages=12, pages=30, page=page, tokens=T, Hq=Hq, Hkv=Hkv, d=d, dtype=F32)
+    eng.Kcache.fill_(float("nan"))
+    eng.Vcache.fill_(float("nan"))
+    hist, length = [np.zeros((2, 0, Hkv, d)) for _ in range(3)], np.zeros(3, int)
+    for at, new in ((None, [40, 1, 0]), (None, [30, 1, 33]), (None, [1, 1, 1]), ([50, -1, 20], [2, 70, 3]),
+                    (None, [3, 0, 76])):
+        for s, a in enumerate(at or ()):
+            if a >= 0:
+                length[s], hist[s] = a, hist[s][:, :a]
+        fused = torch.from_numpy(r.randn(T, Hq + 2 * Hkv, d)).to(DEV).to(F32)
+        Q, K, V = fused[:, :Hq], fused[:, Hq:Hq + Hkv], fused[:, Hq + Hkv:]
+        eng.plan(_i32(length), _i32(new))
+        out = np64(eng.attend(Q, K, V, 0.125))
+        rows = np.concatenate([[0], np.cumsum(new)])
+        assert eng.kv_len.tolist() == (length + new).tolist()
+        for s in range(3):
+            a, b = rows[s], rows[s + 1]
+            hist[s] = np.concatenate([hist[s], np.stack([np64(K[a:b]), np64(V[a:b])])], axis=1)
+            length[s] += new[s]
+            if a == b:
+                continue
+            k, v = (x.transpose(1, 0, 2)[None] for x in hist[s])
+            O, A, _ = oracle.paged_attention(np64(Q[a:b]), k, v, [[0]], [0, b - a], [length[s]], 0.125)
+            largest = np.sqrt((np64(Q[a:b]) ** 2).sum(-1)).max() * np.sqrt((k ** 2).sum(-1)).max() * 0.125
+            w = (d + 4) * 2.0 ** -24 * largest + 2.0 ** -21 + length[s] * 2.0 ** -24
+            assert (np.abs(out[a:b] - O) <= 2 * w * A + 2.0 ** -23 * np.abs(O) + 1e-30).all(), (new, s)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_bad_table_entries_leave_the_other_requests_exact(lib, dtype):
+    # entries outside the pool under one request's keys: the others' bits are those without them
+    c = Case([100, 90, 300], [40, 1, 3], 4, 2, 64, 32, dtype, seed=37, poison=False)
+    want = c.run()
+    c.table[0, 1], c.table[0, 2] = 1 << 30, -5
+    out = c.run()
+    torch.cuda.synchronize()
+    assert_no_device_error()
+    assert torch.equal(out[40:], want[40:])
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("pages,width", [(0, 3), (4, 0), (0, 0)])
+def test_no_pages(lib, dtype, pages, width):
+    # a pool or a table without pages holds no key: every row of a request is zero
+    Kc = torch.zeros(pages, 2, 16, 64, device=DEV, dtype=dtype)
+    Q = torch.randn(6, 4, 64, device=DEV).to(dtype)
+    out = torch.full_like(Q, 7.0)
+    bd.paged_attn_fwd(Q, Kc, Kc.clone(), _i32(np.zeros((2, width))), _i32([0, 1, 5]), _i32([9, 40]), 0.125, out=out)
+    torch.cuda.synchronize()
+    assert_no_device_error()
+    assert (out[:5] == 0).all() and (out[5:] == 7.0).all()
