@@ -212,3 +212,22 @@ def test_attention_refuses_a_scale_that_overflows_in_base_2(lib):
                               (3.4e38, bd.SA_ERR_INVALID_ARG)):
             assert lib.sa_paged_attn_fwd(FAKE, 1024, FAKE, FAKE, dtype, sh, FAKE, FAKE, FAKE, 0, scale, FAKE, None, 0,
                                          None) == status, scale
+
+
+def test_binding_refuses_sizes_beyond_32_bits():
+    # sizes that the C struct's fields would cut: a view of one element stands for the large tensor
+    big = (1 << 32) + 4
+    i = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
+    many = lambda t, *s: t[:1].expand(*s)  # noqa: E731
+    x, c = torch.zeros(4, 2, 64), torch.zeros(3, 2, 16, 64)
+    slots = torch.zeros(1, dtype=torch.int64)
+    for call in (lambda: bd.paged_plan(i(2), i(2), i(2), i(2, 3), i(8), i(2), big, 16, slots=many(slots, big)),
+                 lambda: bd.paged_plan(i(2), i(2), i(2), i(2, 3), i(8), i(2), 4, (1 << 32) + 16),
+                 lambda: bd.paged_plan(i(2), i(2), i(2), i(2, 3), many(i(1), big), i(2), 4, 16),
+                 lambda: bd.paged_plan(i(2), i(2), i(2), many(i(1, 1), 2, big), i(8), i(2), 4, 16),
+                 lambda: bd.paged_append(many(x, big, 2, 64), many(x, big, 2, 64), many(slots, big), c, c),
+                 lambda: bd.paged_attn_fwd(many(x, big, 2, 64), c, c, i(2, 3), i(3), i(2), 1.0),
+                 lambda: bd.paged_attn_fwd(x, c, c, many(i(1, 1), 2, big), i(3), i(2), 1.0),
+                 lambda: bd.paged_attn_workspace_size(4, big, 8, 4, 128, 16, 32, 4)):
+        with pytest.raises(ValueError, match="2\\^31"):
+            call()
