@@ -470,11 +470,10 @@ def _paged_rows(t: torch.Tensor, name: str) -> int:
     return s0 if T > 1 else H * d
 
 
-def _paged_shape(S: int, T: int, Hq: int, Hkv: int, d: int, page: int, P: int, max_pages: int) -> PagedShape:
-    """The C struct of the sizes, whose fields would cut one that leaves 32 bits without a word."""
-    if not -1 <= (S | T | Hq | Hkv | d | page | P | max_pages) >> 31 <= 0:
-        raise ValueError("paged cache: every size must be below 2^31")
-    return PagedShape(S, T, Hq, Hkv, d, page, P, max_pages)
+# A field of PagedShape would cut a size that leaves 32 bits without a word.
+# Checked are those that tensors of this card's memory (or plain numbers) can
+# have.
+_TOO_LARGE = "paged cache: every size must be below 2^31"
 
 
 def _paged_call(i: int, stream, fn: str, f, *args):
@@ -520,7 +519,9 @@ def paged_plan(ctx_len: torch.Tensor, new_len: torch.Tensor, held: torch.Tensor,
     (S,), (P,), (rows, width) = ctx_len.shape, free_pages.shape, table.shape
     if rows != S or new_len.shape != (S,) or held.shape != (S,) or free_state.shape != (2,):
         raise ValueError("new_len and held must be [S], table [S, max_pages], free_state [2]")
-    i, shape = ctx_len.get_device(), _paged_shape(S, tokens, 1, 1, 64, page, P, width)
+    if (S | tokens | page | P | width) >> 31 > 0:
+        raise ValueError(_TOO_LARGE)
+    i = ctx_len.get_device()
     if q_start is None:
         q_start = _paged_empty(ctx_len, S + 1, _I32, stream)
     if kv_len is None:
@@ -531,8 +532,8 @@ def paged_plan(ctx_len: torch.Tensor, new_len: torch.Tensor, held: torch.Tensor,
         raise ValueError("q_start must be [S + 1], kv_len [S], slots [tokens]")
     ptr = _paged_ptr
     _paged_call(i, stream, "sa_paged_plan", load().sa_paged_plan, ptr(ctx_len, i, _I32, "ctx_len"),
-                ptr(new_len, i, _I32, "new_len"), shape, ptr(held, i, _I32, "held"),
-                ptr(table, i, _I32, "table"), ptr(free_pages, i, _I32, "free_pages"),
+                ptr(new_len, i, _I32, "new_len"), PagedShape(S, tokens, 1, 1, 64, page, P, width),
+                ptr(held, i, _I32, "held"), ptr(table, i, _I32, "table"), ptr(free_pages, i, _I32, "free_pages"),
                 ptr(free_state, i, _I32, "free_state"), ptr(q_start, i, _I32, "q_start"),
                 ptr(kv_len, i, _I32, "kv_len"), ptr(slots, i, _I64, "slots"))
     return q_start, kv_len, slots
@@ -547,14 +548,19 @@ def paged_append(K: torch.Tensor, V: torch.Tensor, slots: torch.Tensor, Kcache: 
     T = rows[0]
     if rows != (T, Hkv, d) or V.shape != rows or Vcache.shape != Kcache.shape or slots.shape != (T,):
         raise ValueError("K and V must be [T,Hkv,d], slots [T], the caches [P,Hkv,page,d]")
-    i, dt, ptr, shape = Kcache.get_device(), Kcache.dtype, _paged_ptr, _paged_shape(0, T, Hkv, Hkv, d, page, P, 0)
+    if T >> 31:
+        raise ValueError(_TOO_LARGE)
+    i, dt, ptr = Kcache.get_device(), Kcache.dtype, _paged_ptr
     _paged_call(i, stream, "sa_paged_append", load().sa_paged_append, ptr(K, i, dt, "K", False),
-                ptr(V, i, dt, "V", False), _paged_rows(K, "K"), _paged_rows(V, "V"), _dtype_code(Kcache), shape,
-                ptr(slots, i, _I64, "slots"), ptr(Kcache, i, dt, "Kcache"), ptr(Vcache, i, dt, "Vcache"))
+                ptr(V, i, dt, "V", False), _paged_rows(K, "K"), _paged_rows(V, "V"), _dtype_code(Kcache),
+                PagedShape(0, T, Hkv, Hkv, d, page, P, 0), ptr(slots, i, _I64, "slots"), ptr(Kcache, i, dt, "Kcache"),
+                ptr(Vcache, i, dt, "Vcache"))
 
 
 def paged_attn_workspace_size(S: int, T: int, Hq: int, Hkv: int, d: int, page: int, P: int, max_pages: int) -> int:
-    return int(load().sa_paged_attn_workspace_size(_paged_shape(S, T, Hq, Hkv, d, page, P, max_pages)))
+    if max(S, T, Hq, Hkv, d, page, P, max_pages) >> 31 > 0:
+        raise ValueError(_TOO_LARGE)
+    return int(load().sa_paged_attn_workspace_size(PagedShape(S, T, Hq, Hkv, d, page, P, max_pages)))
 
 
 def paged_attn_fwd(Q: torch.Tensor, Kcache: torch.Tensor, Vcache: torch.Tensor, table: torch.Tensor,
@@ -573,12 +579,14 @@ def paged_attn_fwd(Q: torch.Tensor, Kcache: torch.Tensor, Vcache: torch.Tensor, 
         raise ValueError("q_start must be [S + 1], kv_len [S], table [S, max_pages]")
     if not 0 <= window < 1 << 31:
         raise ValueError("window must be 0 (none) or a number of keys below 2^31")
+    if (T | width) >> 31:
+        raise ValueError(_TOO_LARGE)
     i, dt, ptr, lib = Q.get_device(), Q.dtype, _paged_ptr, load()
-    shape = _paged_shape(S, T, Hq, Hkv, d, page, P, width)
     if out is None:
         out = _paged_empty(Q, (T, Hq, d), dt, stream)
     elif out.shape != Q.shape:
         raise ValueError("out must have Q's shape")
+    shape = PagedShape(S, T, Hq, Hkv, d, page, P, width)
     if workspace is None:
         workspace = _paged_empty(Q, max(lib.sa_paged_attn_workspace_size(shape), 256), _U8, stream)
     _paged_call(i, stream, "sa_paged_attn_fwd", lib.sa_paged_attn_fwd, ptr(Q, i, dt, "Q", False), _paged_rows(Q, "Q"),
