@@ -26,7 +26,9 @@ namespace paged {
 
 constexpr int kMaxRequests = 4096;
 
-// Division of 0 <= n < 2^31 by a divisor that the host knows: a multiplication.
+// Division of 0 <= n < 2^31 by a divisor that the host knows, as a
+// multiplication (the method with a rounded-up reciprocal of Granlund and
+// Montgomery, "Division by invariant integers using multiplication", 1994).
 struct FastDiv {
   uint32_t d, mul, shift;
   explicit FastDiv(uint32_t divisor) : d(divisor), mul(1), shift(0) {
@@ -292,8 +294,10 @@ struct Walker {
 
 // ---- host side
 struct Limits {
-  static constexpr int kCtas = 148;        // CTAs of the tensor-core kernel: one per SM
-  static constexpr int kCtasSimt = 296;    // CTAs of the CUDA-core kernel: two per SM
+  // One or two CTAs on each of B200's 148 SMs (right on any other number, where
+  // some CTAs would wait for a place)
+  static constexpr int kCtas = 148;        // of the tensor-core kernel: one per SM
+  static constexpr int kCtasSimt = 296;    // of the CUDA-core kernel: two per SM
 };
 
 }  // namespace paged

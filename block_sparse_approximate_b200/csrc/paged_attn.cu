@@ -69,8 +69,13 @@ struct Job {
 // scores of two CTAs, shared memory's rate.  Here the D / 4 lanes that copy a
 // row of K or V are the ones that use it, each its own four channels, so the
 // groups of lanes run through their keys without a barrier, each with a
-// running maximum, sum and output of its own (joined once an item), and
-// memory is the bound (32 sequences, 8 / 2 heads of 128: 117 -> 48 us).
+// running maximum, sum and output of its own (joined once an item).  32
+// sequences of about 1900 keys, 2 KV heads of 128: 42 us with up to 4 rows an
+// item, 48 with 5 to 8, against 96 in the tiling above; heads of 64: 22 and 27
+// against 52.  At 42 us memory runs at 52% of the copy rate (19 us would be all
+// of it) and the schedulers issue in 47% of their cycles: the bound is the
+// latency of a CTA's one tile of K and V, refilled once it is consumed, under
+// the 16 warps of an SM.
 //   scores: a lane's products of KB keys and R rows, KB R = the group's lanes,
 //   are summed over the group by halving: lanes exchange half of what they
 //   hold, and lane x ends with the sum of pair reversed(x) = key R + row.

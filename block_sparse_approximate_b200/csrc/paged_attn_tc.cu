@@ -441,8 +441,12 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
     // alone, and they are not stored).  A tile of few tokens (decoding) takes
     // its tokens one by one and keeps the other rows zero: the MMAs multiply
     // them all the same, and with zeros the tensor cores draw so much less
-    // power that a long run of decoding steps holds a higher clock (416 -> 388
-    // us for 128 sequences once the card is at its power limit).
+    // power that a long run of decoding steps holds a higher clock.  Measured
+    // on 128 sequences of up to 8192 keys in such a run, 32 / 8 heads: 401 -> 380 us
+    // with 1 token a tile, 403 -> 389 with 4, 441 -> 416 with 5, 455 -> 441
+    // with 16, 475 either way with 32.  Against that stand the loads of short
+    // batches (16 sequences of 2000 keys): 44 -> 46 us with 4 tokens, 45 -> 47
+    // with 16.  The limit of 4 is single tokens and short drafts.
     int loads = 0;                             // bit h: parity of the loads of query tile h
     int dirty[2] = {0, 0};                     // rows of each tile that may not be zero
     bool ok = warp_wait(bar(L::B_QZ), 0, abort_flag);
@@ -688,7 +692,10 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
           // the tile's own maximum is formed for a row's first keys, for masked
           // tiles and when that check fails (as it does for NaN and inf), and
           // otherwise the exponentials of a quarter of the row run while the
-          // next quarter comes from TMEM (6% of the kernel).  All of them run
+          // next quarter comes from TMEM (6% of the kernel).  Where the check
+          // fails in every tile (scores that rise by 12 binary orders each 128
+          // keys) the second pass makes the chunk of 4096 rows over 16001 keys
+          // 36% slower and decoding 64 sequences 19%.  All exponentials run
           // on MUFU: a share of 1/8 or 3/8 on the FMA pipe, as the block-sparse
           // kernel has, cost 1 and 3%, since the MMA issuer shares that pipe's
           // scheduler.

@@ -195,7 +195,11 @@ class PagedServing:
                              self.page, q_start=self.q_start, kv_len=self.kv_len, slots=self.slots, stream=stream)
 
     def attend(self, Q, K, V, scale: float, *, window: int = 0, caches=None, out=None, stream=None):
-        """Appends the planned step's K, V and attends from Q; ``caches``: another layer's (Kcache, Vcache)."""
+        """Appends the planned step's K, V and attends from Q; ``caches``: another layer's (Kcache, Vcache).
+
+        Q, K and V have ``tokens`` rows, padding included.  Without ``out`` the result is ``self.out``, which the
+        next call overwrites; its rows behind the last request's are left as they were.
+        """
         Kc, Vc = caches if caches is not None else (self.Kcache, self.Vcache)
         bd.paged_append(K, V, self.slots, Kc, Vc, stream=stream)
         return bd.paged_attn_fwd(Q, Kc, Vc, self.table, self.q_start, self.kv_len, scale, window=window,

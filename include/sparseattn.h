@@ -429,10 +429,11 @@ sa_status sa_sfa_attn_fwd(const void* Qs, const void* Ks, const void* V, sa_dtyp
  * three calls can be captured into a graph and replayed with other lengths.
  *
  * S <= 4096 requests; page in {16, 32, 64, 128}; d in {64, 128}; Hq any
- * multiple of Hkv (up to 128 times in bf16); max_pages * page <= 2^30; S * max_pages, P * Hkv and
- * T * Hkv below 2^31, T * Hq <= 2^30 (else SA_ERR_UNSUPPORTED).  Lengths,
- * tables, slots and the free ring are read on the device and bounded there:
- * whatever they hold, nothing outside the given arrays is read or written. */
+ * multiple of Hkv (up to 128 times in bf16); max_pages * page <= 2^30;
+ * S * max_pages, P * Hkv and T * Hkv below 2^31, T * Hq <= 2^30 (else
+ * SA_ERR_UNSUPPORTED).  Lengths, tables, slots and the free ring are read on
+ * the device and bounded there: whatever they hold, nothing outside the given
+ * arrays is read or written. */
 typedef struct {
   int32_t S;          /* requests                                     */
   int32_t T;          /* rows of the packed arrays (padding included) */
@@ -475,7 +476,8 @@ sa_status sa_paged_plan(const int32_t* ctx_len, const int32_t* new_len, sa_paged
  * their slots: Kcache[slot / page][h][slot % page][:] = K[t][h][:], V alike.
  * Rows whose slot lies outside [0, P * page) are skipped.  The slots of a
  * call should differ; of rows with the same slot any one's values may remain,
- * element by element.  Hq of the shape is not used.
+ * element by element.  The caches overlap no other array.  Hq of the shape is
+ * not used.
  * Errors: SA_ERR_INVALID_ARG (null array, a stride below Hkv * d),
  *         SA_ERR_UNSUPPORTED, SA_ERR_ALIGNMENT (16 bytes for tensors and row
  *         strides, 8 for slots). */
