@@ -56,7 +56,7 @@ def _peaks():
 # sources change the figure no longer describes the kernel and is reported as
 # null until it is captured again.
 ATTN_TRAFFIC = {"sources": ("csrc/attn_tc.cu", "csrc/tc_util.cuh", "csrc/common.cuh"),
-                "sha256": "d73ebb7f 77c2c6eb 20b529c1", "bytes": 386.42e6}
+                "sha256": "8d9d409d aaf72200 36135109", "bytes": 389.45e6}
 
 
 def attn_traffic_bytes():

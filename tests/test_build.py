@@ -75,3 +75,9 @@ def test_a_kernel_that_fails_the_check_is_not_linked_by_building_again(small_tre
         with pytest.raises(RuntimeError, match="160 registers"):
             bld.build()
     assert os.listdir(bld.BUILD) == ["paged_attn_tc.o"]
+
+
+def test_bench_traffic_figure_describes_the_present_kernel():
+    # the DRAM bytes of the attention kernel were captured on the sources as they are (bench.py reports null otherwise)
+    import bench
+    assert bench.attn_traffic_bytes() is not None
