@@ -261,3 +261,67 @@ def test_no_pages(lib, dtype, pages, width):
     torch.cuda.synchronize()
     assert_no_device_error()
     assert (out[:5] == 0).all() and (out[5:] == 7.0).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_calls_without_rows_or_requests(lib, dtype):
+    Kc = torch.ones(3, 2, 16, 64, device=DEV, dtype=dtype)
+    before = Kc.clone()
+    none = torch.empty(0, 2, 64, device=DEV, dtype=dtype)
+    bd.paged_append(none, none, torch.empty(0, device=DEV, dtype=torch.int64), Kc, Kc.clone())
+    assert torch.equal(Kc, before)
+    table, kv = _i32([[0, 1]]), _i32([20])
+    assert bd.paged_attn_fwd(none, Kc, Kc, table, _i32([0, 0]), kv, 0.125).shape == (0, 2, 64)
+    out = torch.full((3, 2, 64), 7.0, device=DEV, dtype=dtype)
+    bd.paged_attn_fwd(torch.ones_like(out), Kc, Kc, _i32(np.zeros((0, 2))), _i32([0]), _i32([]), 0.125, out=out)
+    assert (out == 7.0).all()
+    # a plan without rows in its arrays still hands pages back, and refuses rows
+    held, ring, state = _i32([2]), _i32([2, 0, 0]), _i32([0, 1])
+    q_start, kv_len, slots = bd.paged_plan(_i32([5]), _i32([0]), held, table, ring, state, 0, 16)
+    assert q_start.tolist() == [0, 0] and kv_len.tolist() == [5] and held.tolist() == [1] and slots.numel() == 0
+    assert table.tolist() == [[0, -1]] and state.tolist() == [0, 2] and ring.tolist()[:2] == [2, 1]
+    assert bd.paged_plan(_i32([5]), _i32([1]), held, table, ring, state, 0, 16)[1].tolist() == [0]
+
+
+def test_many_requests_captured(lib):
+    # plan, append and fp32 attention of 2440 requests in a graph, replayed with other lengths
+    S, page, T = 2440, 16, 2600
+    r = np.random.RandomState(38)
+    eng = PagedServing(requests=S, max_pages=3, pages=2 * S, page=page, tokens=T, Hq=2, Hkv=1, d=64, dtype=F32)
+    ctx_d, new_d = _i32(np.zeros(S)), _i32(np.zeros(S))
+    fused = torch.zeros(T, 4, 64, device=DEV)
+    Q, K, V = fused[:, :2], fused[:, 2:3], fused[:, 3:]
+
+    def step():
+        eng.plan(ctx_d, new_d)
+        eng.attend(Q, K, V, 0.125)
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        step()                                      # nothing to do yet: lengths are zero
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    length, rows = np.zeros(S, int), [[np.zeros((0, 64))] * 2 for _ in range(S)]
+    for _ in range(3):
+        new = r.randint(0, 2, S)
+        new[r.randint(0, S, 20)] = r.randint(2, 12, 20)
+        ctx_d.copy_(_i32(length))
+        new_d.copy_(_i32(new))
+        fused.copy_(torch.from_numpy(r.randn(T, 4, 64)).to(DEV))
+        g.replay()
+        out, q, k, v = (np64(x) for x in (eng.out, Q, K, V))
+        assert eng.kv_len.tolist() == (length + new).tolist()
+        q_start = np.concatenate([[0], np.cumsum(new)])
+        length += new
+        for s in range(S):
+            a, b = q_start[s], q_start[s + 1]
+            rows[s] = [np.concatenate([x, y[a:b, 0]]) for x, y in zip(rows[s], (k, v))]
+            if a == b:
+                continue
+            O, A, _ = oracle.paged_attention(q[a:b], *(x[None, None] for x in rows[s]), [[0]], [0, b - a], [length[s]],
+                                             0.125)
+            largest = np.sqrt((q[a:b] ** 2).sum(-1)).max() * np.sqrt((rows[s][0] ** 2).sum(-1)).max() * 0.125
+            w = 68 * 2.0 ** -24 * largest + 2.0 ** -21 + length[s] * 2.0 ** -24
+            assert (np.abs(out[a:b] - O) <= 2 * w * A + 2.0 ** -23 * np.abs(O) + 1e-30).all(), s
+    assert_no_device_error()
